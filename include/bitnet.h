@@ -120,6 +120,11 @@ extern "C" {
  * other sizes or on the results' tolerance. */
 #define BITNET_FFN_SINGLE_LAUNCH 0x200
 
+/* ------------------------------------------------- rotary embedding flags */
+#define BITNET_ROPE_HALF         0     /* pairs (i, i + rot_dim / 2)                */
+#define BITNET_ROPE_INTERLEAVED  0x1   /* pairs (2 i, 2 i + 1)                      */
+#define BITNET_ROPE_HEAD_NORM    0x2   /* RMSNorm of every query and key head first */
+
 typedef void *bitnet_stream_t;       /* a cudaStream_t */
 
 #if defined(BITNET_BUILD) && defined(__GNUC__)
@@ -246,6 +251,94 @@ BITNET_API int bitnet_linear_multi(const int8_t *Xq, const float *x_scale,
                                    const uint8_t *const *packed, const float *const *gamma,
                                    const int *N, int M, int K, void *const *Y, int epilogue,
                                    bitnet_stream_t stream);
+
+/* The product of two int8 matrices with a scale per token and per output
+ * channel, for the layers of a model that are not ternary (an 8-bit output
+ * head, first or last blocks).  The codes of both sides are those of
+ * bitnet_quant_act() without a prelude: a weight matrix [N][K] is quantised as
+ * N rows, once, and its x_scale is the w_scale here.
+ *   Xq, x_scale   [M][K] codes and [M] scales s = 127 / max|x| of the tokens
+ *   Wq, w_scale   [N][K] codes and [N] scales of the output channels
+ *   Y         out: [M][N] of the type in (epilogue & BITNET_EPI_TYPE_MASK):
+ *             y = acc / (x_scale[m] * w_scale[n]) with the exact int32 sum acc
+ *             (three further fp32 roundings), then the optional SiLU and
+ *             residual as bitnet_linear(); BITNET_I32 writes acc itself.
+ *   residual  [M][N] of Y's type when BITNET_EPI_RESIDUAL is set, else NULL.
+ * Scales must be nonzero.  Y may be residual's buffer.  The launch hints are
+ * not taken.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+BITNET_API int bitnet_linear_w8(const int8_t *Xq, const float *x_scale, const int8_t *Wq,
+                                const float *w_scale, int M, int N, int K, void *Y, int epilogue,
+                                const void *residual, bitnet_stream_t stream);
+
+/* Paged key/value cache (nnterp "bitnet", "Printout": 20 query and 5 key/value
+ * heads of 128): the step between the q/k/v projections and o_proj.
+ *   k_cache, v_cache  [num_pages][kv_heads][page_size][head_dim], bf16.
+ *   block_table  [batch][table_stride] int32: position j of sequence b lives in
+ *             page block_table[b][j / page_size] at slot j % page_size.  Only
+ *             the entries of pages that hold cached tokens are read.
+ *   cu_q      [batch + 1] int32, cu_q[0] = 0, not falling: rows cu_q[b] ..
+ *             cu_q[b + 1] - 1 of the token rows are the new tokens of sequence
+ *             b (none is allowed).  Rows from cu_q[batch] to M are padding:
+ *             nothing of them is read as a token or written.
+ *   kv_len    [batch] int32: tokens of sequence b once its new tokens are
+ *             appended.  New token i of n is at position kv_len - n + i; one
+ *             at a negative position has no place and is left out.
+ * q_heads is a multiple of kv_heads; query head h reads key/value head
+ * h / (q_heads / kv_heads).  head_dim is a multiple of 16 in [16, 256],
+ * page_size a multiple of 16, table_stride * page_size at most 2^30.  The
+ * tables are device memory read on the stream, so a captured call follows
+ * lengths that change between replays.  A page index, row or length out of
+ * range is recorded in the device error word (bitnet_check_device_error()
+ * returns INVALID_ARG); no access is made there and the outputs of that
+ * sequence are unspecified.
+ *
+ * Rotate the new tokens' queries and keys and append keys and values.
+ *   Q, K, V   token rows [M] of q_heads, kv_heads, kv_heads heads of `dtype`
+ *             (F32 or BF16); *_stride elements between rows (whole 16-byte
+ *             units; a fused projection's row stride is taken as it is).
+ *   inv_freq  [rot_dim / 2] fp32: pair i of a token at position p turns by
+ *             p * inv_freq[i], the angle formed in fp64.  rot_dim is a
+ *             multiple of 16 up to head_dim; the rest of a head passes.
+ *   flags     BITNET_ROPE_*.  HEAD_NORM: x * g / sqrt(mean(x^2) + eps) over
+ *             each head before the rotation, q_gain and k_gain [head_dim] fp32
+ *             or NULL for all ones.
+ *   Q_out     out: [M][q_heads * head_dim] of `dtype`, contiguous; may be Q
+ *             itself when Q's rows are.  Rows without a place keep their
+ *             contents.  Keys and values are rounded to bf16 once.
+ * The slots appended to must be distinct.  Errors: INVALID_ARG, CUDA. */
+BITNET_API int bitnet_rope_append(const void *Q, int64_t q_stride, const void *K,
+                                  int64_t k_stride, const void *V, int64_t v_stride, int dtype,
+                                  int M, int q_heads, int kv_heads, int head_dim,
+                                  const float *inv_freq, int rot_dim, int flags,
+                                  const float *q_gain, const float *k_gain, float eps, int batch,
+                                  const int32_t *cu_q, const int32_t *kv_len,
+                                  const int32_t *block_table, int table_stride, void *k_cache,
+                                  void *v_cache, int num_pages, int page_size, void *Q_out,
+                                  bitnet_stream_t stream);
+
+/* Workspace bytes bitnet_attention() needs for calls of at most M token rows
+ * and `batch` sequences. */
+BITNET_API size_t bitnet_attention_workspace_size(int M, int batch, int q_heads, int kv_heads,
+                                                  int head_dim);
+
+/* Causal attention of the new tokens over the cache that holds them already
+ * (after bitnet_rope_append()): one token per sequence, chunks of prompts and
+ * whole prompts, mixed as cu_q says.
+ *   Q, O      [M][q_heads * head_dim] of `dtype` (F32 or BF16), contiguous
+ *   scale     factor of the scores (1 / sqrt(head_dim) in the model)
+ * The token at position p attends to positions 0 .. p of its sequence; one
+ * with none (a negative position) gives zeros.  Scores, softmax statistics and
+ * sums are fp32; BF16 calls round the probabilities to bf16 before their
+ * product with V, F32 calls carry them in 16 bits and Q in 24.  Slots past a
+ * sequence's length may hold anything, NaN included.  The workspace needs no
+ * initialisation; calls that share one must not overlap on the GPU.  O must
+ * not overlap Q.  Errors: INVALID_ARG, WORKSPACE, CUDA. */
+BITNET_API int bitnet_attention(const void *Q, int dtype, int M, int q_heads, int kv_heads,
+                                int head_dim, float scale, int batch, const int32_t *cu_q,
+                                const int32_t *kv_len, const int32_t *block_table,
+                                int table_stride, const void *k_cache, const void *v_cache,
+                                int num_pages, int page_size, void *O, void *workspace,
+                                size_t ws_bytes, bitnet_stream_t stream);
 
 /* Workspace bytes bitnet_ffn() needs. */
 BITNET_API size_t bitnet_ffn_workspace_size(int M, int H, int I, int variant);

@@ -11,6 +11,9 @@ Functions carry the C names and take torch tensors plus explicit outputs:
     bitnet_pack_weights(W, packed, gamma, workspace)
     bitnet_quant_act(X, Xq, x_scale, x_rowsum, prelude=..., norm_gain=None, eps=1e-5)
     bitnet_linear(Xq, x_scale, x_rowsum, packed, gamma, K, Y, epilogue=..., residual=None)
+    bitnet_linear_w8(Xq, x_scale, Wq, w_scale, Y, silu=False, residual=None)
+    bitnet_rope_append(Q, K, V, inv_freq, cu_q, kv_len, block_table, k_cache, v_cache, Q_out, ...)
+    bitnet_attention(Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspace, scale=None)
     bitnet_ffn(X, W_gate, gamma_gate, W_up, gamma_up, W_down, gamma_down, Y, workspace, ...)
 
 ``alloc_*`` helpers size the outputs with torch.
@@ -41,11 +44,17 @@ from ._binding import (  # noqa: F401
     BITNET_PRELUDE_FWHT,
     BITNET_PRELUDE_NONE,
     BITNET_PRELUDE_RMSNORM,
+    BITNET_ROPE_HALF,
+    BITNET_ROPE_HEAD_NORM,
+    BITNET_ROPE_INTERLEAVED,
     BitnetError,
+    alloc_attention_workspace,
     alloc_block_tail_workspace,
     alloc_ffn_workspace,
     alloc_packed,
     alloc_quant,
+    bitnet_attention,
+    bitnet_attention_workspace_size,
     bitnet_block_tail,
     bitnet_block_tail_workspace_size,
     bitnet_check_device_error,
@@ -59,12 +68,14 @@ from ._binding import (  # noqa: F401
     bitnet_import_tw2,
     bitnet_linear,
     bitnet_linear_multi,
+    bitnet_linear_w8,
     bitnet_pack_weights,
     bitnet_pack_workspace_size,
     bitnet_packed_row_bytes,
     bitnet_plan_linear,
     bitnet_quant_act,
     bitnet_release_cache,
+    bitnet_rope_append,
     bitnet_version,
     library,
     library_path,

@@ -23,6 +23,7 @@ BITNET_LAUNCH_PDL = 0x100
 BITNET_LAUNCH_PDL_INPUTS = 0x200
 BITNET_FFN_RELU2_GLU, BITNET_FFN_HADAMARD_SILU = 0, 1
 BITNET_FFN_SINGLE_LAUNCH = 0x200
+BITNET_ROPE_HALF, BITNET_ROPE_INTERLEAVED, BITNET_ROPE_HEAD_NORM = 0, 1, 2
 (BITNET_PLAN_STREAM, BITNET_PLAN_FLAT, BITNET_PLAN_GEMV_TC, BITNET_PLAN_GEMV,
  BITNET_PLAN_GEMM_TC) = 1, 2, 3, 4, 5
 
@@ -53,6 +54,7 @@ def library():
                           "(the BitLinear path has no CPU fallback)")
     lib = ctypes.CDLL(path)
     P, I, U, S, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t, ctypes.c_float
+    L = ctypes.c_int64
     sigs = {
         "bitnet_packed_row_bytes": (S, [I]),
         "bitnet_pack_workspace_size": (S, [I, I]),
@@ -69,6 +71,11 @@ def library():
         "bitnet_block_tail_workspace_size": (S, [I, I, I]),
         "bitnet_block_tail": (I, [P, P, I, I, I, I, P, P, P, P, P, P, P, P, P, P, P, F, P, P, P,
                                   S, P]),
+        "bitnet_linear_w8": (I, [P, P, P, P, I, I, I, P, I, P, P]),
+        "bitnet_rope_append": (I, [P, L, P, L, P, L, I, I, I, I, I, P, I, I, P, P, F, I, P, P, P,
+                                   I, P, P, I, I, P, P]),
+        "bitnet_attention_workspace_size": (S, [I, I, I, I, I]),
+        "bitnet_attention": (I, [P, I, I, I, I, I, F, I, P, P, P, I, P, P, I, I, P, P, S, P]),
         "bitnet_last_error": (ctypes.c_char_p, []),
         "bitnet_check_device_error": (I, [P]),
         "bitnet_debug_wait_timeout": (I, [U, P]),
@@ -244,6 +251,133 @@ def bitnet_block_tail(A, X, W_o, gamma_o, W_gate, gamma_gate, W_up, gamma_up, W_
 def alloc_block_tail_workspace(M, H, I, device="cuda"):
     return torch.empty(max(1, bitnet_block_tail_workspace_size(M, H, I)), dtype=torch.uint8,
                        device=device)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _one_device(stream, **tensors):
+    """Every tensor on one CUDA device, the current one: the launch goes there."""
+    current = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        _need(t.is_cuda, f"{name} must live on a CUDA device")
+        _need(t.device.index == current,
+              f"{name} is on {t.device}, the current device is cuda:{current}")
+
+
+def _int32(name, t, *shape):
+    _need(t.dtype == torch.int32 and tuple(t.shape) == shape,
+          f"{name} must be int32 of shape {list(shape)}")
+
+
+def _rows(name, t, width, dtype):
+    """Pointer and row stride of a matrix whose rows are contiguous."""
+    _need(t.dim() == 2 and t.shape[1] == width and t.dtype == dtype,
+          f"{name} must be [M][{width}] of {dtype}")
+    _need(t.shape[1] == 1 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (width if t.shape[0] <= 1 else t.stride(0))
+
+
+def _paged(cu_q, kv_len, block_table, k_cache, v_cache):
+    """(batch, table_stride, num_pages, kv_heads, page_size, head_dim) of a paged cache."""
+    _need(k_cache.dim() == 4 and k_cache.dtype == torch.bfloat16 and
+          v_cache.dtype == torch.bfloat16 and k_cache.shape == v_cache.shape,
+          "k_cache and v_cache must be bf16 [num_pages][kv_heads][page_size][head_dim]")
+    batch = kv_len.numel()
+    _int32("kv_len", kv_len, batch)
+    _int32("cu_q", cu_q, batch + 1)
+    _need(block_table.dim() == 2, "block_table must be [batch][table_stride]")
+    _int32("block_table", block_table, batch, block_table.shape[1])
+    pages, heads, page, dim = k_cache.shape
+    return batch, block_table.shape[1], pages, heads, page, dim
+
+
+def _gain(name, t, dim):
+    if t is not None:
+        _need(t.dtype == torch.float32 and t.numel() == dim, f"{name} must be fp32 [{dim}]")
+    return _ptr(t)
+
+
+def bitnet_linear_w8(Xq, x_scale, Wq, w_scale, Y, silu=False, residual=None, epilogue=None,
+                     stream=None):
+    """Y [M][N] = (Xq . Wq^T) / (x_scale[m] w_scale[n]) (int32 Y: the sum itself), the codes
+    and scales of both sides from bitnet_quant_act (see include/bitnet.h)."""
+    _one_device(stream, Xq=Xq, x_scale=x_scale, Wq=Wq, w_scale=w_scale, Y=Y, residual=residual)
+    _need(Xq.dim() == 2 and Wq.dim() == 2 and Xq.dtype == Wq.dtype == torch.int8 and
+          Xq.shape[1] == Wq.shape[1], "Xq and Wq must be int8 [M][K] and [N][K]")
+    (M, K), N = Xq.shape, Wq.shape[0]
+    _need(x_scale.dtype == w_scale.dtype == torch.float32 and x_scale.numel() == M and
+          w_scale.numel() == N, "x_scale and w_scale must be fp32 [M] and [N]")
+    _need(tuple(Y.shape) == (M, N), f"Y must be [{M}][{N}]")
+    if residual is not None:
+        _need(residual.shape == Y.shape and residual.dtype == Y.dtype,
+              "residual must have Y's shape and type")
+    if epilogue is None:
+        epilogue = (_dtype(Y) | (BITNET_EPI_SILU if silu else 0) |
+                    (BITNET_EPI_RESIDUAL if residual is not None else 0))
+    _need((epilogue & BITNET_EPI_TYPE_MASK) == _dtype(Y), "epilogue names another type than Y's")
+    _check(library().bitnet_linear_w8(_ptr(Xq), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), M, N, K,
+                                      _ptr(Y), int(epilogue), _ptr(residual), _stream(stream)))
+
+
+def bitnet_rope_append(Q, K, V, inv_freq, cu_q, kv_len, block_table, k_cache, v_cache, Q_out,
+                       rope=BITNET_ROPE_HALF, head_norm=False, q_gain=None, k_gain=None, eps=1e-5,
+                       stream=None):
+    """Rotate the new tokens' queries (into Q_out) and keys and append keys and values to the
+    paged cache (see include/bitnet.h).  Q, K, V are [M][heads * head_dim]; their rows may be
+    strided (slices of one fused projection)."""
+    _one_device(stream, Q=Q, K=K, V=V, inv_freq=inv_freq, cu_q=cu_q, kv_len=kv_len,
+                block_table=block_table, k_cache=k_cache, v_cache=v_cache, Q_out=Q_out,
+                q_gain=q_gain, k_gain=k_gain)
+    batch, stride, pages, heads, page, dim = _paged(cu_q, kv_len, block_table, k_cache, v_cache)
+    M, width = Q.shape
+    q, ldq = _rows("Q", Q, width, Q.dtype)
+    k, ldk = _rows("K", K, heads * dim, Q.dtype)
+    v, ldv = _rows("V", V, heads * dim, Q.dtype)
+    _need(width % dim == 0 and K.shape[0] == V.shape[0] == M,
+          "Q, K and V must have the same rows, of whole heads")
+    _need(Q_out.shape == Q.shape and Q_out.dtype == Q.dtype, "Q_out must have Q's shape and type")
+    _need(inv_freq.dtype == torch.float32, "inv_freq must be fp32")
+    flags = int(rope) | (BITNET_ROPE_HEAD_NORM if head_norm else 0)
+    _check(library().bitnet_rope_append(
+        q, ldq, k, ldk, v, ldv, _dtype(Q), M, width // dim, heads, dim, _ptr(inv_freq),
+        2 * inv_freq.numel(), flags, _gain("q_gain", q_gain, dim), _gain("k_gain", k_gain, dim),
+        float(eps), batch, _ptr(cu_q), _ptr(kv_len), _ptr(block_table), stride, _ptr(k_cache),
+        _ptr(v_cache), pages, page, _ptr(Q_out), _stream(stream)))
+
+
+def bitnet_attention_workspace_size(M, batch, q_heads, kv_heads, head_dim):
+    return int(library().bitnet_attention_workspace_size(int(M), int(batch), int(q_heads),
+                                                         int(kv_heads), int(head_dim)))
+
+
+def alloc_attention_workspace(M, batch, q_heads, kv_heads, head_dim, device="cuda"):
+    """Workspace of bitnet_attention for calls of at most M rows and `batch` sequences."""
+    return torch.empty(max(1, bitnet_attention_workspace_size(M, batch, q_heads, kv_heads,
+                                                              head_dim)),
+                       dtype=torch.uint8, device=device)
+
+
+def bitnet_attention(Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspace, scale=None,
+                     stream=None):
+    """Causal attention of the new tokens over the paged cache (see include/bitnet.h); scale is
+    1 / sqrt(head_dim) unless given."""
+    _one_device(stream, Q=Q, cu_q=cu_q, kv_len=kv_len, block_table=block_table, k_cache=k_cache,
+                v_cache=v_cache, O=O, workspace=workspace)
+    batch, stride, pages, heads, page, dim = _paged(cu_q, kv_len, block_table, k_cache, v_cache)
+    _need(Q.dim() == 2 and Q.shape[1] % dim == 0, "Q must be [M][q_heads * head_dim]")
+    _need(O.shape == Q.shape and O.dtype == Q.dtype, "O must have Q's shape and type")
+    if scale is None:
+        scale = dim ** -0.5
+    _check(library().bitnet_attention(
+        _ptr(Q), _dtype(Q), Q.shape[0], Q.shape[1] // dim, heads, dim, float(scale), batch,
+        _ptr(cu_q), _ptr(kv_len), _ptr(block_table), stride, _ptr(k_cache), _ptr(v_cache), pages,
+        page, _ptr(O), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
 
 
 BITNET_FFN_NOALLOC_SCRATCH_BYTES = 8 << 20

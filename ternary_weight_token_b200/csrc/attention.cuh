@@ -1,0 +1,671 @@
+// attention.cuh -- causal attention of the new tokens of a batch over their
+// paged key/value cache: work plan, the mma.sync kernel, and the join of
+// split sequences.
+//
+// nnterp encyclopedia "bitnet", "Printout": 20 query heads over 5 key/value
+// heads of 128.
+//
+// Row r of sequence b at position p sees keys 0 .. p of its own sequence:
+//   o = sum_j softmax_j(scale q . k_j) v_j,
+// computed in one pass with a running maximum m and sum l (fp32):
+//   m' = max(m, z_j), l' = l 2^(m - m') + sum 2^(z_j - m'), o' likewise,
+// with z in units of log2 (scale * log2 e folded into one factor).  A row
+// that sees no key gives zeros.
+//
+// The query heads that share a key/value head are rows of one tile: row
+// t * G + g of a sequence is token t, head g of the group, so a tile reads
+// its keys and values once for all of them.
+//
+// Work: a tile of rows (RT) times one key/value head is an item; where the
+// batch has too few items to fill the GPU its keys are cut into splits of at
+// least `min_units` blocks, sized on the device from the lengths it finds
+// there (so a captured graph keeps fitting as the cache grows).  A split
+// writes its unnormalised sums and statistics to the workspace and the join
+// kernel adds them; an uncut item writes its rows directly.
+#pragma once
+
+#include "common.cuh"
+#include "rope_append.cuh"
+
+namespace bitnet {
+
+constexpr int kAttnThreads = 128;
+constexpr int kAttnTile = 64;          // keys per block of the mma.sync kernel
+constexpr int kAttnTarget = 592;       // splits wanted over a call: four per SM
+constexpr int kAttnPlanHead = 4;       // words before the per-sequence slots of the plan
+
+struct AttnParams {
+  PagedBatch pb;
+  const void* Q;
+  void* O;
+  const __nv_bfloat16 *Kc, *Vc;
+  int qh, kvh, G, D;
+  float scale_log2;                    // softmax scale * log2(e)
+  int RT;                              // rows per tile
+  int unit;                            // keys per block
+  int min_units;                       // smallest split, in blocks
+  int target;                          // splits wanted over the whole call, 0: never split
+  int* plan;                           // [0] blocks per split, [kAttnPlanHead + b] first slot of b
+  float* part;                         // slots: m[RT], l[RT], o[RT][D]
+};
+
+// --------------------------------------------------------------- the plan
+struct SeqWork {
+  int c0, n, len;                      // first row, new tokens, cached tokens
+  int tiles, units;
+};
+
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool report) {
+  SeqWork w;
+  w.c0 = __ldg(p.pb.cu_q + b);
+  const int c1 = __ldg(p.pb.cu_q + b + 1);
+  w.len = __ldg(p.pb.kv_len + b);
+  const long long cap = (long long)p.pb.stride * p.pb.page_size;
+  if (w.c0 < 0 || c1 < w.c0 || c1 > p.pb.M) {
+    if (report) record_device_error(DEV_ERR_INDEX);
+    w.c0 = 0;
+    w.n = 0;
+  } else {
+    w.n = c1 - w.c0;
+  }
+  if (w.len < 0 || w.len > cap) {
+    if (report) record_device_error(DEV_ERR_INDEX);
+    w.len = w.len < 0 ? 0 : (int)cap;
+  }
+  w.tiles = (int)(((long long)w.n * p.G + p.RT - 1) / p.RT);
+  w.units = (w.len + p.unit - 1) / p.unit;
+  return w;
+}
+
+__device__ __forceinline__ int splits_of(int units, int chunk) {
+  return units <= chunk ? 1 : (units + chunk - 1) / chunk;
+}
+
+// Thread t of the CTA holds sequences [t per, (t + 1) per) of the batch.
+struct PlanShared {
+  int chunk, total;
+  int items[kAttnThreads + 1];         // items before each thread's sequences
+  int slots[kAttnThreads + 1];
+  long long red[kAttnThreads / 32];
+  // the item that was looked up
+  int b, local, splits, slot;
+  SeqWork w;
+};
+
+// Inclusive scan over the first kAttnThreads threads' values (two at a time).
+__device__ __forceinline__ void plan_scan(int& a, int& b, PlanShared& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int o = 1; o < 32; o *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += x;
+      b += y;
+    }
+  }
+  if (lane == 31) s.red[warp] = ((long long)b << 32) | (unsigned)a;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) {
+    a += (int)(s.red[i] & 0xffffffffll);
+    b += (int)(s.red[i] >> 32);
+  }
+}
+
+// All kAttnThreads threads of the CTA.
+__device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
+  const int tid = threadIdx.x, B = p.pb.batch;
+  const int per = (B + kAttnThreads - 1) / kAttnThreads;
+  const int b0 = tid * per, b1 = min(B, b0 + per);
+  const bool first = blockIdx.x == 0;
+  int chunk = 0x7fffffff;
+  if (p.target > 0) {
+    long long u = 0;
+    for (int b = b0; b < b1; ++b) {
+      const SeqWork w = seq_work(p, b, false);
+      u += (long long)w.tiles * w.units;
+    }
+    for (int o = 16; o > 0; o /= 2) u += __shfl_xor_sync(0xffffffffu, u, o);
+    if ((tid & 31) == 0) s.red[tid >> 5] = u;
+    __syncthreads();
+    u = 0;
+    for (int i = 0; i < kAttnThreads / 32; ++i) u += s.red[i];
+    const long long want = (u * p.kvh + p.target - 1) / p.target;
+    chunk = want < p.min_units ? p.min_units : want > 0x7ffffffell ? 0x7fffffff : (int)want;
+    __syncthreads();
+  }
+  int items = 0, slots = 0;
+  for (int b = b0; b < b1; ++b) {
+    const SeqWork w = seq_work(p, b, first);
+    const int sp = splits_of(w.units, chunk);
+    items += w.tiles * p.kvh * sp;
+    if (sp > 1) slots += w.tiles * p.kvh * sp;
+  }
+  const int mine = items, mine_s = slots;
+  plan_scan(items, slots, s);
+  s.items[tid] = items - mine;
+  s.slots[tid] = slots - mine_s;
+  if (tid == kAttnThreads - 1) {
+    s.items[kAttnThreads] = items;
+    s.total = items;
+    s.chunk = chunk;
+  }
+  if (first && p.target > 0) {         // for the join kernel
+    if (tid == 0) p.plan[0] = chunk;
+    int at = slots - mine_s;
+    for (int b = b0; b < b1; ++b) {
+      const SeqWork w = seq_work(p, b, false);
+      const int sp = splits_of(w.units, chunk);
+      p.plan[kAttnPlanHead + b] = at;
+      if (sp > 1) at += w.tiles * p.kvh * sp;
+    }
+  }
+  __syncthreads();
+}
+
+// Sequence of item c, and its place there.  All kAttnThreads threads.
+__device__ __forceinline__ void find_item(const AttnParams& p, PlanShared& s, int c) {
+  const int tid = threadIdx.x;
+  if (c >= s.items[tid] && c < s.items[tid + 1]) {
+    const int per = (p.pb.batch + kAttnThreads - 1) / kAttnThreads;
+    const int b1 = min(p.pb.batch, (tid + 1) * per);
+    int at = s.items[tid], slot = s.slots[tid];
+    s.b = -1;                          // kept only if the lengths changed under the call
+    for (int b = tid * per; b < b1; ++b) {
+      const SeqWork w = seq_work(p, b, false);
+      const int sp = splits_of(w.units, s.chunk);
+      const int k = w.tiles * p.kvh * sp;
+      if (c < at + k) {
+        s.b = b;
+        s.w = w;
+        s.local = c - at;
+        s.splits = sp;
+        s.slot = sp > 1 ? slot + (c - at) : -1;
+        break;
+      }
+      at += k;
+      if (sp > 1) slot += k;
+    }
+  }
+  __syncthreads();
+}
+
+// Item `local` of a sequence: its tile, key/value head and split.  Late tiles
+// see the most keys, so they come first.
+__device__ __forceinline__ void item_place(const AttnParams& p, const SeqWork& w, int local,
+                                           int splits, int& tile, int& head, int& split) {
+  split = local % splits;
+  const int i = local / splits;
+  head = i % p.kvh;
+  tile = w.tiles - 1 - i / p.kvh;
+}
+
+// ------------------------------------------------------------ instructions
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool take) {
+  const int n = take ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ------------------------------------------------------- mma.sync kernel
+// Four warps: WR of them along the rows (16 each), 4 / WR along the keys of a
+// block.  WR = 1 is the decode form: 16 rows, each warp its own quarter of
+// every block with its own statistics, joined in shared memory at the end.
+// WR = 4 takes 64 rows of a chunk.
+//
+// fp32 queries (F32): q is held as three bf16 terms (24 bits, exact) and the
+// probabilities as two (16 bits, 2^-17 relative), so products with the bf16
+// cache carry fp32-like accuracy for 3 + 2 instead of 1 + 1 matrix products.
+// bf16 queries round the probabilities to bf16 (2^-9 relative, averaged over
+// the keys, below the rounding of the output); l sums the unrounded ones.
+template <int DP, int WR, bool F32>
+struct AttnConfig {
+  static constexpr int RT = 16 * WR;
+  static constexpr int WK = 4 / WR;
+  static constexpr int KW = kAttnTile / WK;          // keys of a warp per block
+  static constexpr int STAGES = DP == 64 ? 4 : DP == 128 ? 3 : 2;
+  static constexpr int TERMS = F32 ? 3 : 1;
+  static constexpr int ROW = DP * 2;                 // bytes of a staged row
+  static constexpr int Q_BYTES = RT * ROW * TERMS;
+  static constexpr int KV_BYTES = kAttnTile * ROW;
+  static constexpr int PAGE_TILES = 128;             // blocks whose page offsets are staged
+  static constexpr int OFF_KV = Q_BYTES;
+  static constexpr int OFF_PAGES = OFF_KV + STAGES * 2 * KV_BYTES;
+  static constexpr int SMEM = OFF_PAGES + PAGE_TILES * (kAttnTile / 16) * 8;
+  static constexpr bool Q_REGS = !F32 && DP <= 128;
+  static_assert(WK * RT * DP * 4 <= STAGES * 2 * KV_BYTES || WR == 4, "join buffer");
+};
+
+// 16-byte chunk c of staged row r.
+template <int ROW>
+__device__ __forceinline__ uint32_t attn_at(uint32_t base, int r, int c) {
+  return base + (uint32_t)(r * ROW + ((c ^ (r & 7)) << 4));
+}
+
+template <int DP, int WR, bool F32>
+__global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
+  using C = AttnConfig<DP, WR, F32>;
+  extern __shared__ __align__(1024) uint8_t attn_smem[];
+  __shared__ PlanShared plan;
+  __shared__ float s_m[4][16], s_l[4][16];
+  const uint32_t sq = smem_u32(attn_smem), skv = sq + C::OFF_KV;
+  long long* s_off = reinterpret_cast<long long*>(attn_smem + C::OFF_PAGES);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int wr = WR == 1 ? 0 : warp, wk = WR == 1 ? warp : 0;
+  const int D = p.D, chunks = D / 8;
+
+  grid_launch_dependents();
+  grid_dependency_wait();
+  make_plan(p, plan);
+
+  for (int c = blockIdx.x; c < plan.total; c += gridDim.x) {
+    find_item(p, plan, c);
+    const SeqWork w = plan.w;
+    const int splits = plan.splits, slot = plan.slot, b = plan.b;
+    if (b < 0) {
+      __syncthreads();
+      continue;
+    }
+    int tile, head, split;
+    item_place(p, w, plan.local, splits, tile, head, split);
+    const int rows = w.n * p.G;                      // of the whole sequence
+    const int row0 = tile * C::RT;
+    const int nrows = min(C::RT, rows - row0);
+    const int past = w.len - w.n;                    // tokens before the new ones (may be < 0)
+    const int kv_end = max(0, past + (row0 + nrows - 1) / p.G + 1);
+    const int lim_first = past + row0 / p.G + 1;     // keys that the first row sees
+    const int blocks = (kv_end + kAttnTile - 1) / kAttnTile;
+    const int blk0 = (int)((long long)blocks * split / splits);
+    const int blk1 = (int)((long long)blocks * (split + 1) / splits);
+
+    // ---- queries to shared memory (zeros past the rows and past D)
+    for (int i = tid; i < C::RT * (DP / 8); i += kAttnThreads) {
+      const int r = i / (DP / 8), ch = i % (DP / 8);
+      const bool ok = r < nrows && ch < chunks;
+      const int rr = row0 + (ok ? r : 0);
+      const long long off =
+          ((long long)(w.c0 + rr / p.G) * p.qh + (long long)head * p.G + rr % p.G) * D + 8 * ch;
+      uint4 u[C::TERMS];
+#pragma unroll
+      for (int t = 0; t < C::TERMS; ++t) u[t] = make_uint4(0, 0, 0, 0);
+      if (ok) {
+        if constexpr (F32) {
+          const float* src = reinterpret_cast<const float*>(p.Q) + off;
+          float x[8];
+          *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+          *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(src + 4);
+#pragma unroll
+          for (int t = 0; t < 3; ++t) {
+            uint32_t wds[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              wds[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+              x[2 * k] -= __uint_as_float(wds[k] << 16);
+              x[2 * k + 1] -= __uint_as_float(wds[k] & 0xffff0000u);
+            }
+            u[t] = make_uint4(wds[0], wds[1], wds[2], wds[3]);
+          }
+        } else {
+          u[0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.Q) + off);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < C::TERMS; ++t)
+        *reinterpret_cast<uint4*>(attn_smem + (attn_at<C::ROW>(sq, r, ch) - sq) +
+                                  t * C::RT * C::ROW) = u[t];
+    }
+
+    // ---- keys and values: a ring of blocks filled by cp.async
+    auto load = [&](int i) {
+      const int blk = blk0 + i;
+      if (i % C::PAGE_TILES == 0) {                  // page offsets of the next blocks
+        __syncthreads();
+        for (int k = tid; k < C::PAGE_TILES * 4; k += kAttnThreads) {
+          const int key = blk * kAttnTile + 16 * k;  // capacities stay below 2^30
+          long long off = -1;
+          if (blk + k / 4 < blk1 && key < kv_end) {
+            const int page = __ldg(p.pb.table + (long long)b * p.pb.stride + key / p.pb.page_size);
+            if (page < 0 || page >= p.pb.num_pages)
+              record_device_error(DEV_ERR_INDEX);
+            else
+              off = (((long long)page * p.kvh + head) * p.pb.page_size + key % p.pb.page_size) * D;
+          }
+          s_off[k] = off;
+        }
+        __syncthreads();
+      }
+      if (blk < blk1) {
+        const uint32_t dst = skv + (uint32_t)((i % C::STAGES) * 2 * C::KV_BYTES);
+        const int g0 = (i % C::PAGE_TILES) * 4;
+#pragma unroll
+        for (int k = 0; k < kAttnTile * (DP / 8) / kAttnThreads; ++k) {
+          const int idx = tid + k * kAttnThreads;
+          const int r = idx / (DP / 8), ch = idx % (DP / 8);
+          const long long base = s_off[g0 + (r >> 4)];
+          // keys past the end may be anything, NaN too: zeros take their place
+          const bool ok = base >= 0 && blk * kAttnTile + r < kv_end && ch < chunks;
+          const long long off = ok ? base + (long long)(r & 15) * D + 8 * ch : 0;
+          cp_async_16(attn_at<C::ROW>(dst, r, ch), p.Kc + off, ok);
+          cp_async_16(attn_at<C::ROW>(dst + C::KV_BYTES, r, ch), p.Vc + off, ok);
+        }
+      }
+      cp_async_commit();
+    };
+
+    const int count = blk1 - blk0;
+#pragma unroll 1
+    for (int i = 0; i < C::STAGES - 1; ++i) load(i);
+
+    float o[DP / 8][4];
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int lim[2];                                      // keys that this thread's rows see
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = 16 * wr + (lane >> 2) + 8 * k;
+      lim[k] = r < nrows ? past + (row0 + r) / p.G + 1 : 0;
+    }
+    uint32_t qf[C::Q_REGS ? DP / 16 : 1][4];
+
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      cp_async_wait<C::STAGES - 2>();
+      __syncthreads();
+      if constexpr (C::Q_REGS) {
+        if (i == 0) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k)
+            ldmatrix_x4(attn_at<C::ROW>(sq, 16 * wr + (lane & 15), 2 * k + (lane >> 4)), qf[k]);
+        }
+      }
+      load(i + C::STAGES - 1);
+      const uint32_t sk = skv + (uint32_t)((i % C::STAGES) * 2 * C::KV_BYTES);
+      const uint32_t sv = sk + C::KV_BYTES;
+      float z[C::KW / 8][4];
+#pragma unroll
+      for (int n = 0; n < C::KW / 8; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[n][k] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k) {
+        uint32_t a[C::TERMS][4];
+        if constexpr (C::Q_REGS) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) a[0][x] = qf[k][x];
+        } else {
+#pragma unroll
+          for (int t = 0; t < C::TERMS; ++t)
+            ldmatrix_x4(attn_at<C::ROW>(sq + t * C::RT * C::ROW, 16 * wr + (lane & 15),
+                                        2 * k + (lane >> 4)), a[t]);
+        }
+#pragma unroll
+        for (int n = 0; n < C::KW / 16; ++n) {
+          uint32_t kb[4];
+          ldmatrix_x4(attn_at<C::ROW>(sk, C::KW * wk + 16 * n + (lane & 7) + ((lane >> 4) << 3),
+                                      2 * k + ((lane >> 3) & 1)), kb);
+#pragma unroll
+          for (int t = C::TERMS - 1; t >= 0; --t) {  // smallest terms first
+            mma_bf16(z[2 * n], a[t], kb[0], kb[1]);
+            mma_bf16(z[2 * n + 1], a[t], kb[2], kb[3]);
+          }
+        }
+      }
+      const int key0 = (blk0 + i) * kAttnTile + C::KW * wk + 2 * (lane & 3);
+      const bool masked = (blk0 + i + 1) * kAttnTile > lim_first || nrows < C::RT;
+      float mx[2] = {m[0], m[1]};
+#pragma unroll
+      for (int n = 0; n < C::KW / 8; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float v = z[n][k] * p.scale_log2;
+          if (masked && key0 + 8 * n + (k & 1) >= lim[k >> 1]) v = -INFINITY;
+          z[n][k] = v;
+          mx[k >> 1] = fmaxf(mx[k >> 1], v);
+        }
+      float alpha[2], base[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+        base[k] = mx[k] == -INFINITY ? 0.0f : mx[k];  // nothing seen yet: all terms are 0
+        alpha[k] = ex2(m[k] - base[k]);
+        m[k] = mx[k];
+        l[k] *= alpha[k];
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n) {
+          o[n][0] *= alpha[0];
+          o[n][1] *= alpha[0];
+          o[n][2] *= alpha[1];
+          o[n][3] *= alpha[1];
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < C::KW / 16; ++n) {
+        float e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          e[k] = ex2(z[2 * n + (k >> 2)][k & 3] - base[(k >> 1) & 1]);
+          l[(k >> 1) & 1] += e[k];
+        }
+        uint32_t ph[4], pl[4];
+        ph[0] = pack_bf16x2(e[0], e[1]);
+        ph[1] = pack_bf16x2(e[2], e[3]);
+        ph[2] = pack_bf16x2(e[4], e[5]);
+        ph[3] = pack_bf16x2(e[6], e[7]);
+        if constexpr (F32) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            pl[k] = pack_bf16x2(e[2 * k] - __uint_as_float(ph[k] << 16),
+                                e[2 * k + 1] - __uint_as_float(ph[k] & 0xffff0000u));
+        }
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+          uint32_t v0, v1, v2, v3;
+          ldmatrix_x4_trans(attn_at<C::ROW>(sv, C::KW * wk + 16 * n + (lane & 15),
+                                            2 * d + (lane >> 4)), v0, v1, v2, v3);
+          if constexpr (F32) {
+            mma_bf16(o[2 * d], pl, v0, v1);
+            mma_bf16(o[2 * d + 1], pl, v2, v3);
+          }
+          mma_bf16(o[2 * d], ph, v0, v1);
+          mma_bf16(o[2 * d + 1], ph, v2, v3);
+        }
+      }
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+    }
+
+    float* part = slot >= 0 ? p.part + (long long)slot * C::RT * (D + 2) : nullptr;
+    auto store2 = [&](int r, int d, float x, float y) {
+      if (slot >= 0) {
+        *reinterpret_cast<float2*>(part + 2 * C::RT + r * D + d) = make_float2(x, y);
+        return;
+      }
+      const int rr = row0 + r;
+      const long long off =
+          ((long long)(w.c0 + rr / p.G) * p.qh + (long long)head * p.G + rr % p.G) * D + d;
+      if constexpr (F32)
+        *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.O) + off) = make_float2(x, y);
+      else
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.O) + off) =
+            pack_bf16x2(x, y);
+    };
+    if constexpr (WR == 1) {
+      // the four warps' sums, each relative to the rows' common maximum
+      __syncthreads();                               // the ring is free
+      if ((lane & 3) == 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          s_m[warp][(lane >> 2) + 8 * k] = m[k];
+          s_l[warp][(lane >> 2) + 8 * k] = l[k];
+        }
+      }
+      __syncthreads();
+      float* so = reinterpret_cast<float*>(attn_smem + C::OFF_KV);   // [4][16][DP]
+      float f[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = (lane >> 2) + 8 * k;
+        const float mm = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+        f[k] = mm == -INFINITY ? 0.0f : ex2(m[k] - mm);
+      }
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<float2*>(so + (warp * 16 + (lane >> 2) + 8 * k) * DP + 8 * n +
+                                     2 * (lane & 3)) =
+              make_float2(o[n][2 * k] * f[k], o[n][2 * k + 1] * f[k]);
+      __syncthreads();
+      for (int i = tid; i < 16 * (D / 2); i += kAttnThreads) {
+        const int r = i / (D / 2), d = 2 * (i % (D / 2));
+        if (r >= nrows) break;
+        const float mm = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+        float sum = 0.0f, x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          sum += mm == -INFINITY ? 0.0f : s_l[q][r] * ex2(s_m[q][r] - mm);
+          const float2 v = *reinterpret_cast<const float2*>(so + (q * 16 + r) * DP + d);
+          x += v.x;
+          y += v.y;
+        }
+        if (slot >= 0) {
+          if (d == 0) {
+            part[r] = mm;
+            part[C::RT + r] = sum;
+          }
+          store2(r, d, x, y);
+        } else {
+          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+          store2(r, d, x * inv, y * inv);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = 16 * wr + (lane >> 2) + 8 * k;
+        if (r < nrows) {
+          float inv = l[k] > 0.0f ? 1.0f / l[k] : 0.0f;
+          if (slot >= 0) {
+            inv = 1.0f;
+            if ((lane & 3) == 0) {
+              part[r] = m[k];
+              part[C::RT + r] = l[k];
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < DP / 8; ++n)
+            if (8 * n < D)
+              store2(r, 8 * n + 2 * (lane & 3), o[n][2 * k] * inv, o[n][2 * k + 1] * inv);
+        }
+      }
+    }
+    __syncthreads();                                 // plan, ring and statistics are free
+  }
+}
+
+// --------------------------------------------------------------- the join
+// One CTA per token row and query head.  Its split count comes from the
+// lengths and the blocks per split that the attention kernel left in the
+// plan; warps take the splits in turn, lanes the D values.
+template <bool F32>
+__global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
+  __shared__ float s_o[4][kRopeMaxDim];
+  __shared__ float s_ml[4][2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int r = blockIdx.x, qhead = blockIdx.y;
+  const int b = sequence_of(p.pb, r, lane);
+  if (b >= p.pb.batch) return;
+  const SeqWork w = seq_work(p, b, false);
+  if (w.n == 0 || r < w.c0) return;
+  const int splits = splits_of(w.units, p.plan[0]);
+  if (splits == 1) return;
+  const int head = qhead / p.G;
+  const int row = (r - w.c0) * p.G + qhead % p.G;
+  const int tile = row / p.RT, rt = row % p.RT;
+  const long long slot0 = (long long)p.plan[kAttnPlanHead + b] +
+                          ((long long)(w.tiles - 1 - tile) * p.kvh + head) * splits;
+  const long long size = (long long)p.RT * (p.D + 2);
+  const float* part = p.part + slot0 * size;
+  const int per = p.D / 8;                           // 8 values per lane, up to 32 lanes
+  float m = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int s = warp; s < splits; s += 4) m = fmaxf(m, part[s * size + rt]);
+  if (m != -INFINITY) {
+#pragma unroll 4
+    for (int s = warp; s < splits; s += 4) {
+      const float* q = part + s * size;
+      const float f = ex2(q[rt] - m);
+      l += f * q[p.RT + rt];
+      if (lane < per) {
+        const float4* v = reinterpret_cast<const float4*>(q + 2 * p.RT + rt * p.D + 8 * lane);
+        const float4 x = v[0], y = v[1];
+        o[0] += f * x.x; o[1] += f * x.y; o[2] += f * x.z; o[3] += f * x.w;
+        o[4] += f * y.x; o[5] += f * y.y; o[6] += f * y.z; o[7] += f * y.w;
+      }
+    }
+  }
+  if (lane == 0) {
+    s_ml[warp][0] = m;
+    s_ml[warp][1] = l;
+  }
+  if (lane < per) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s_o[warp][8 * lane + k] = o[k];
+  }
+  __syncthreads();
+  float mm = -INFINITY, sum = 0.0f, f[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mm = fmaxf(mm, s_ml[k][0]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[k] = mm == -INFINITY ? 0.0f : ex2(s_ml[k][0] - mm);
+    sum += f[k] * s_ml[k][1];
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  for (int d = tid; d < p.D; d += kAttnThreads) {
+    const float x = inv * (f[0] * s_o[0][d] + f[1] * s_o[1][d] + f[2] * s_o[2][d] +
+                           f[3] * s_o[3][d]);
+    const long long off = ((long long)r * p.qh + qhead) * p.D + d;
+    if (F32)
+      reinterpret_cast<float*>(p.O)[off] = x;
+    else
+      reinterpret_cast<__nv_bfloat16*>(p.O)[off] = __float2bfloat16_rn(x);
+  }
+}
+
+}  // namespace bitnet

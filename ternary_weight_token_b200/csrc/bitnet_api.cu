@@ -21,13 +21,16 @@
 #include <unordered_map>
 
 #include "../../include/bitnet.h"
+#include "attention.cuh"
 #include "common.cuh"
 #include "ffn_decode.cuh"
 #include "gemm_tc.cuh"
 #include "gemv.cuh"
 #include "gemv_tc.cuh"
+#include "linear_w8.cuh"
 #include "pack_weights.cuh"
 #include "quant_act.cuh"
+#include "rope_append.cuh"
 
 namespace bitnet {
 namespace {
@@ -179,6 +182,20 @@ constexpr size_t kMapCacheMax = 16384;   // descriptors (128 B each) kept at mos
 std::mutex g_map_mu;
 std::unordered_map<MapKey, CUtensorMap, MapKeyHash> g_map_cache;
 
+// Tensor map of `rank` dimensions; strides[i] is that of dimension i + 1.
+int encode_map(CUtensorMap& out, const void* ptr, CUtensorMapDataType dtype, int rank,
+               const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+               CUtensorMapSwizzle swz) {
+  EncodeTiledFn enc = nullptr;
+  if (int rc = get_encode_fn(enc)) return rc;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(&out, dtype, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(BITNET_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return BITNET_OK;
+}
+
 // 2-D tensor [d1 rows][d0 elements] of `dtype` with row stride `stride` bytes,
 // box [b1 rows][b0 elements].
 int tensor_map_2d(CUtensorMap& out, const void* ptr, CUtensorMapDataType dtype, uint64_t d0,
@@ -196,16 +213,10 @@ int tensor_map_2d(CUtensorMap& out, const void* ptr, CUtensorMapDataType dtype, 
       return BITNET_OK;
     }
   }
-  EncodeTiledFn enc = nullptr;
-  if (int rc = get_encode_fn(enc)) return rc;
   cuuint64_t dims[2] = {d0, d1};
   cuuint64_t strides[1] = {stride};
   cuuint32_t box[2] = {b0, b1};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(&out, dtype, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(BITNET_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  if (int rc = encode_map(out, ptr, dtype, 2, dims, strides, box, swz)) return rc;
   std::lock_guard<std::mutex> lock(g_map_mu);
   // bounded: a caller that keeps passing new buffers starts the cache over
   // instead of growing it without limit
@@ -830,6 +841,101 @@ int launch_ffn_decode(FfnDecodeParams p, cudaStream_t st, bool tail = false) {
   return BITNET_OK;
 }
 
+// ---------------------------------------------- paged cache and attention
+int validate_paged(int dtype, int M, int q_heads, int kv_heads, int head_dim, int batch,
+                   int table_stride, int num_pages, int page_size) {
+  if (dtype != BITNET_F32 && dtype != BITNET_BF16)
+    return fail(BITNET_ERR_INVALID_ARG, "dtype must be F32 or BF16");
+  if (M < 0 || batch < 0)
+    return fail(BITNET_ERR_INVALID_ARG, "M=%d, batch=%d must be >= 0", M, batch);
+  if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || q_heads > 65535)
+    return fail(BITNET_ERR_INVALID_ARG,
+                "q_heads=%d must be a multiple of kv_heads=%d, at most 65535", q_heads, kv_heads);
+  if (head_dim < 16 || head_dim > kRopeMaxDim || head_dim % 16 != 0)
+    return fail(BITNET_ERR_INVALID_ARG, "head_dim=%d must be a multiple of 16 in [16, %d]",
+                head_dim, kRopeMaxDim);
+  if (page_size < 16 || page_size % 16 != 0 || num_pages < 1 || table_stride < 1)
+    return fail(BITNET_ERR_INVALID_ARG,
+                "page_size=%d must be a positive multiple of 16, num_pages=%d and "
+                "table_stride=%d positive", page_size, num_pages, table_stride);
+  if ((long long)table_stride * page_size > (1ll << 30))
+    return fail(BITNET_ERR_INVALID_ARG, "table_stride * page_size must be at most 2^30");
+  if ((long long)num_pages * kv_heads > 0x7fffffffll)
+    return fail(BITNET_ERR_INVALID_ARG, "num_pages * kv_heads must be below 2^31");
+  if ((long long)M * q_heads > 0x7fffffffll)
+    return fail(BITNET_ERR_INVALID_ARG, "M * q_heads must be below 2^31");
+  return BITNET_OK;
+}
+
+// Row tile and split target of an attention call (pure host logic).
+struct AttnShape {
+  int RT, unit, min_units, target;
+};
+
+AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim) {
+  const int G = q_heads / kv_heads;
+  AttnShape sh;
+  // tiles of 16 rows while a sequence has that many on average, else of 64;
+  // heads wider than 128 do not leave the registers for 64
+  sh.RT = (long long)M * G <= 16ll * batch || head_dim > 128 ? 16 : 64;
+  sh.unit = kAttnTile;
+  sh.min_units = 4;
+  sh.target = kAttnTarget;
+  // enough items without splitting
+  if ((long long)M * G / sh.RT * kv_heads >= 2 * kAttnTarget) sh.target = 0;
+  return sh;
+}
+
+template <int DP, int WR, bool F32>
+int launch_attn_rows(const AttnParams& p, int sms, cudaStream_t st) {
+  using C = AttnConfig<DP, WR, F32>;
+  void (*kern)(AttnParams) = attn_rows_kernel<DP, WR, F32>;
+  if (int rc = set_smem_attr((const void*)kern, C::SMEM)) return rc;
+  int per_sm = 0;
+  if (int rc = occupancy(per_sm, (const void*)kern, kAttnThreads, C::SMEM)) return rc;
+  const long long items =
+      ((long long)p.pb.M * p.G / C::RT + p.pb.batch) * p.kvh + p.target;   // at most
+  const long long cap = (long long)sms * (per_sm < 1 ? 1 : per_sm);
+  return launch_pdl(kern, dim3((unsigned)std::min(items, cap)), dim3(kAttnThreads), C::SMEM, st, p);
+}
+
+template <int WR, bool F32>
+int launch_attn_dim(const AttnParams& p, int sms, cudaStream_t st) {
+  if (p.D <= 64) return launch_attn_rows<64, WR, F32>(p, sms, st);
+  if (p.D <= 128) return launch_attn_rows<128, WR, F32>(p, sms, st);
+  if constexpr (WR == 1) return launch_attn_rows<256, WR, F32>(p, sms, st);
+  return BITNET_ERR_UNSUPPORTED;                     // attn_shape() keeps these at 16 rows
+}
+
+template <class C>
+int launch_w8_cfg(const W8Params& params, const int8_t* Xq, const int8_t* Wq, int K,
+                  cudaStream_t st) {
+  DeviceInfo di;
+  if (int rc = device_info(di)) return rc;
+  W8Params p = params;
+  CUtensorMap mx, mw;
+  const cuuint64_t stride[1] = {(cuuint64_t)K};
+  const cuuint64_t dx[2] = {(cuuint64_t)K, (cuuint64_t)p.M}, dw[2] = {(cuuint64_t)K, (cuuint64_t)p.N};
+  const cuuint32_t bx[2] = {C::BK, C::BN}, bw[2] = {C::BK, C::BM};
+  if (int rc = encode_map(mx, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dx, stride, bx,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+    return rc;
+  if (int rc = encode_map(mw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dw, stride, bw,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+    return rc;
+  p.num_kb = (K + C::BK - 1) / C::BK;
+  p.tiles_n = (p.N + C::BM - 1) / C::BM;
+  const long long tiles = (long long)p.tiles_n * ((p.M + C::BN - 1) / C::BN);
+  if (tiles > 0x7fffffffll - di.sms) return fail(BITNET_ERR_UNSUPPORTED, "too many output tiles");
+  p.num_tiles = (int)tiles;
+  // one CTA per SM (tensor memory): too much shared memory for two
+  const size_t smem = std::max((size_t)C::SMEM_ALLOC, (size_t)di.max_smem_optin / 2 + 1024);
+  auto kern = linear_w8_kernel<C>;
+  if (int rc = set_smem_attr((const void*)kern, smem)) return rc;
+  const int grid = p.num_tiles < di.sms ? p.num_tiles : di.sms;
+  return launch_pdl(kern, dim3(grid), dim3(C::THREADS), smem, st, mx, mw, p);
+}
+
 int validate_linear(const int8_t* Xq, const float* xs, const int32_t* xrs, const uint8_t* W,
                     const float* gamma, int M, int N, int K, const void* Y, int epilogue,
                     const void* resid) {
@@ -1339,6 +1445,157 @@ int bitnet_block_tail(const void* A, const void* X, int dtype, int M, int H, int
   return rc;
 }
 
+int bitnet_linear_w8(const int8_t* Xq, const float* x_scale, const int8_t* Wq,
+                     const float* w_scale, int M, int N, int K, void* Y, int epilogue,
+                     const void* residual, bitnet_stream_t stream) {
+  g_last_error.clear();
+  if (epilogue & (BITNET_LAUNCH_PDL | BITNET_LAUNCH_PDL_INPUTS))
+    return fail(BITNET_ERR_INVALID_ARG, "unknown epilogue flags 0x%x", epilogue);
+  // the argument rules of bitnet_linear; there are no code sums, and the
+  // channel scales take the place of the weight scale
+  if (int rc = validate_linear(Xq, x_scale, reinterpret_cast<const int32_t*>(x_scale),
+                               reinterpret_cast<const uint8_t*>(Wq), w_scale, M, N, K, Y, epilogue,
+                               residual))
+    return rc;
+  if (M == 0 || N == 0) return BITNET_OK;
+  W8Params p = {};
+  p.xs = x_scale; p.ws = w_scale; p.Y = Y; p.resid = residual;
+  p.M = M; p.N = N;
+  p.out_type = epilogue & BITNET_EPI_TYPE_MASK;
+  p.flags = epilogue & ~BITNET_EPI_TYPE_MASK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (M <= 16) return launch_w8_cfg<W8Config<16, 10>>(p, Xq, Wq, K, st);
+  if (M <= 32) return launch_w8_cfg<W8Config<32, 9>>(p, Xq, Wq, K, st);
+  if (M <= 64) return launch_w8_cfg<W8Config<64, 8>>(p, Xq, Wq, K, st);
+  if (M <= 128) return launch_w8_cfg<W8Config<128, 6>>(p, Xq, Wq, K, st);
+  return launch_w8_cfg<W8Config<256, 4>>(p, Xq, Wq, K, st);
+}
+
+int bitnet_rope_append(const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
+                       const void* V, int64_t v_stride, int dtype, int M, int q_heads,
+                       int kv_heads, int head_dim, const float* inv_freq, int rot_dim, int flags,
+                       const float* q_gain, const float* k_gain, float eps, int batch,
+                       const int32_t* cu_q, const int32_t* kv_len, const int32_t* block_table,
+                       int table_stride, void* k_cache, void* v_cache, int num_pages,
+                       int page_size, void* Q_out, bitnet_stream_t stream) {
+  g_last_error.clear();
+  if (int rc = validate_paged(dtype, M, q_heads, kv_heads, head_dim, batch, table_stride,
+                              num_pages, page_size))
+    return rc;
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0)
+    return fail(BITNET_ERR_INVALID_ARG, "rot_dim=%d must be a multiple of 16 in [0, head_dim]",
+                rot_dim);
+  if (flags & ~(BITNET_ROPE_INTERLEAVED | BITNET_ROPE_HEAD_NORM))
+    return fail(BITNET_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  const bool norm = (flags & BITNET_ROPE_HEAD_NORM) != 0;
+  if (!norm && (q_gain || k_gain))
+    return fail(BITNET_ERR_INVALID_ARG, "gains are only used with BITNET_ROPE_HEAD_NORM");
+  if (norm && !(eps >= 0.0f && std::isfinite(eps)))
+    return fail(BITNET_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  const long long wq = (long long)q_heads * head_dim, wk = (long long)kv_heads * head_dim;
+  const int per16 = dtype == BITNET_BF16 ? 8 : 4;
+  if (q_stride < wq || k_stride < wk || v_stride < wk || q_stride % per16 || k_stride % per16 ||
+      v_stride % per16)
+    return fail(BITNET_ERR_INVALID_ARG,
+                "row strides must cover a row and be whole 16-byte units");
+  if (M == 0 || batch == 0) return BITNET_OK;
+  const void* need[] = {Q, K, V, cu_q, kv_len, block_table, k_cache, v_cache, Q_out};
+  for (const void* q : need)
+    if (!q) return fail(BITNET_ERR_INVALID_ARG, "null pointer argument");
+  if (rot_dim > 0 && !inv_freq) return fail(BITNET_ERR_INVALID_ARG, "inv_freq is NULL");
+  const void* wide[] = {Q, K, V, k_cache, v_cache, Q_out};
+  for (const void* q : wide)
+    if (!aligned16(q)) return fail(BITNET_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  const void* words[] = {cu_q, kv_len, block_table, inv_freq, q_gain, k_gain};
+  for (const void* q : words)
+    if (q && (reinterpret_cast<uintptr_t>(q) & 3u))
+      return fail(BITNET_ERR_INVALID_ARG, "tables and gains must be 4-byte aligned");
+  if (Q_out == Q && q_stride != wq)
+    return fail(BITNET_ERR_INVALID_ARG, "in place (Q_out == Q) needs contiguous query rows");
+  DeviceInfo di;
+  if (int rc = device_info(di)) return rc;
+  RopeParams p = {};
+  p.pb = {cu_q, kv_len, block_table, batch, table_stride, num_pages, page_size, M};
+  p.Q = Q; p.K = K; p.V = V; p.ldq = q_stride; p.ldk = k_stride; p.ldv = v_stride; p.Qo = Q_out;
+  p.Kc = reinterpret_cast<__nv_bfloat16*>(k_cache);
+  p.Vc = reinterpret_cast<__nv_bfloat16*>(v_cache);
+  p.inv_freq = inv_freq; p.qg = q_gain; p.kg = k_gain; p.eps = eps;
+  p.qh = q_heads; p.kvh = kv_heads; p.D = head_dim; p.rot = rot_dim;
+  p.interleaved = (flags & BITNET_ROPE_INTERLEAVED) ? 1 : 0;
+  p.tokens = M >= di.sms * 16 ? 4 : 1;
+  const bool bf = dtype == BITNET_BF16;
+  void (*kern)(RopeParams) =
+      bf ? (norm ? rope_append_kernel<true, true> : rope_append_kernel<true, false>)
+         : (norm ? rope_append_kernel<false, true> : rope_append_kernel<false, false>);
+  const size_t smem = (size_t)p.tokens * (head_dim / 2) * sizeof(float2);
+  return launch_pdl(kern, dim3((unsigned)((M + p.tokens - 1) / p.tokens)), dim3(kRopeThreads),
+                    smem, reinterpret_cast<cudaStream_t>(stream), p);
+}
+
+size_t bitnet_attention_workspace_size(int M, int batch, int q_heads, int kv_heads,
+                                       int head_dim) {
+  if (M < 0 || batch < 0 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 ||
+      head_dim < 1 || head_dim > kRopeMaxDim)
+    return 0;
+  // the largest that a call of at most M rows and `batch` sequences takes
+  const int rt = (long long)M * (q_heads / kv_heads) <= 16 || head_dim > 128 ? 16 : 64;
+  return align256(((size_t)batch + kAttnPlanHead) * 4) +
+         (size_t)2 * kAttnTarget * rt * (head_dim + 2) * 4;
+}
+
+int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads, int head_dim,
+                     float scale, int batch, const int32_t* cu_q, const int32_t* kv_len,
+                     const int32_t* block_table, int table_stride, const void* k_cache,
+                     const void* v_cache, int num_pages, int page_size, void* O, void* workspace,
+                     size_t ws_bytes, bitnet_stream_t stream) {
+  g_last_error.clear();
+  if (int rc = validate_paged(dtype, M, q_heads, kv_heads, head_dim, batch, table_stride,
+                              num_pages, page_size))
+    return rc;
+  if (!std::isfinite(scale)) return fail(BITNET_ERR_INVALID_ARG, "scale must be finite");
+  if (M == 0 || batch == 0) return BITNET_OK;
+  const void* need[] = {Q, cu_q, kv_len, block_table, k_cache, v_cache, O};
+  for (const void* q : need)
+    if (!q) return fail(BITNET_ERR_INVALID_ARG, "null pointer argument");
+  const void* wide[] = {Q, k_cache, v_cache, O};
+  for (const void* q : wide)
+    if (!aligned16(q)) return fail(BITNET_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  const void* words[] = {cu_q, kv_len, block_table};
+  for (const void* q : words)
+    if (reinterpret_cast<uintptr_t>(q) & 3u)
+      return fail(BITNET_ERR_INVALID_ARG, "tables must be 4-byte aligned");
+  const size_t ws_need = bitnet_attention_workspace_size(M, batch, q_heads, kv_heads, head_dim);
+  if (workspace == nullptr || ws_bytes < ws_need)
+    return fail(BITNET_ERR_WORKSPACE, "workspace of %zu bytes needed", ws_need);
+  if (!aligned16(workspace)) return fail(BITNET_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  DeviceInfo di;
+  if (int rc = device_info(di)) return rc;
+  const AttnShape sh = attn_shape(M, batch, q_heads, kv_heads, head_dim);
+  AttnParams p = {};
+  p.pb = {cu_q, kv_len, block_table, batch, table_stride, num_pages, page_size, M};
+  p.Q = Q; p.O = O;
+  p.Kc = reinterpret_cast<const __nv_bfloat16*>(k_cache);
+  p.Vc = reinterpret_cast<const __nv_bfloat16*>(v_cache);
+  p.qh = q_heads; p.kvh = kv_heads; p.G = q_heads / kv_heads; p.D = head_dim;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.RT = sh.RT; p.unit = sh.unit; p.min_units = sh.min_units; p.target = sh.target;
+  // sequences that cannot hold more than one split never need the join
+  if ((long long)table_stride * page_size <= (long long)sh.min_units * sh.unit) p.target = 0;
+  p.plan = reinterpret_cast<int*>(workspace);
+  p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
+                                    align256(((size_t)batch + kAttnPlanHead) * 4));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool f32 = dtype == BITNET_F32;
+  int rc;
+  if (sh.RT == 16)
+    rc = f32 ? launch_attn_dim<1, true>(p, di.sms, st) : launch_attn_dim<1, false>(p, di.sms, st);
+  else
+    rc = f32 ? launch_attn_dim<4, true>(p, di.sms, st) : launch_attn_dim<4, false>(p, di.sms, st);
+  if (rc || p.target == 0) return rc;
+  return launch_pdl(f32 ? attn_join_kernel<true> : attn_join_kernel<false>,
+                    dim3((unsigned)M, (unsigned)q_heads), dim3(kAttnThreads), 0, st, p);
+}
+
 const char* bitnet_last_error(void) { return g_last_error.c_str(); }
 
 int bitnet_check_device_error(bitnet_stream_t stream) {
@@ -1350,6 +1607,9 @@ int bitnet_check_device_error(bitnet_stream_t stream) {
     BN_CHECK_CUDA(cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)));
     if (word & DEV_ERR_TIMEOUT)
       return fail(BITNET_ERR_TIMEOUT, "a bounded device-side wait gave up (error word 0x%x)", word);
+    if (word & DEV_ERR_INDEX)
+      return fail(BITNET_ERR_INVALID_ARG,
+                  "a page index, token row or length in device memory was out of range");
     return fail(BITNET_ERR_CUDA, "device error word 0x%x", word);
   }
   return BITNET_OK;

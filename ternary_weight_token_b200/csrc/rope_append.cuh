@@ -1,0 +1,300 @@
+// rope_append.cuh -- rotary position embedding of the new tokens' queries and
+// keys, and the append of their keys and values to a paged cache.
+//
+// nnterp encyclopedia "bitnet", "Config" and "Printout": 20 query and 5
+// key/value heads of 128, rotary embedding with theta 500000.
+//
+// For token row r of sequence b at position p, pair i of a head
+//   (x, y) -> (x cos a - y sin a, y cos a + x sin a),  a = p * inv_freq[i],
+// optionally after an RMSNorm of the head (x * g / sqrt(mean(x^2) + eps)).
+// The angle is formed in fp64 (p * inv_freq is exact there: 31 + 24 bits, two
+// of them rounded), reduced to a fraction of a turn, and only the reduced
+// angle is rounded to fp32; norms, rotation and products are fp32, and each
+// output is rounded once.
+//
+// Bound by memory: a token of the 2B model reads 7.5 KB and writes 7.5 KB.  A
+// group of lanes owns one head and moves it in 16-byte loads and stores (eight
+// bf16 or four fp32 pairs per lane); the head's values are loaded before the
+// CTA looks its tokens up and forms their cosines and sines, which all heads
+// of the token then share.
+#pragma once
+
+#include "common.cuh"
+
+namespace bitnet {
+
+// Where the new tokens of a batch of sequences stand, and the pages that hold
+// their past: shared by the append and by the attention that reads the cache.
+struct PagedBatch {
+  const int32_t* cu_q;     // [batch + 1] first token row of each sequence
+  const int32_t* kv_len;   // [batch] tokens in the cache once the new ones are appended
+  const int32_t* table;    // [batch][stride] pages of each sequence
+  int batch, stride;
+  int num_pages, page_size;
+  int M;                   // token rows the caller's tensors have
+};
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxDim = 256;
+
+struct RopeParams {
+  PagedBatch pb;
+  const void *Q, *K, *V;
+  long long ldq, ldk, ldv;          // elements between token rows
+  void* Qo;
+  __nv_bfloat16 *Kc, *Vc;
+  const float* inv_freq;            // [rot / 2]
+  const float *qg, *kg;             // [D] or null
+  float eps;
+  int qh, kvh, D, rot;
+  int interleaved;
+  int tokens;                       // per CTA, at most one per warp
+};
+
+// Sequence of token row r: the number of sequences that end at or before it
+// (every lane of the warp gets it).
+__device__ __forceinline__ int sequence_of(const PagedBatch& pb, int r, int lane) {
+  int b = 0;
+  for (int base = 0; base < pb.batch; base += 128) {
+    int done[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = base + 32 * k + lane;
+      done[k] = i < pb.batch && __ldg(pb.cu_q + i + 1) <= r;
+    }
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) n += __popc(__ballot_sync(0xffffffffu, done[k]));
+    b += n;
+    if (n < 128) break;
+  }
+  return b;
+}
+
+template <bool BF16>
+struct RopeVec;                     // 16 bytes of one head
+template <>
+struct RopeVec<true> {
+  static constexpr int N = 8;
+  __device__ static void unpack(const uint4& u, float* x) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct RopeVec<false> {
+  static constexpr int N = 4;
+  __device__ static void unpack(const uint4& u, float* x) {
+    x[0] = __uint_as_float(u.x);
+    x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z);
+    x[3] = __uint_as_float(u.w);
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// N consecutive elements from fp32 values.
+template <int N>
+__device__ __forceinline__ void store_f32(float* p, const float* x) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+}
+template <int N>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float* x) {
+  if constexpr (N == 8) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                   pack_bf16x2(x[6], x[7]));
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  }
+}
+
+// First element of the two runs of N that lane slot j of a head holds: runs of
+// pairs (first[i], second[i]) when the pairs are split in halves, one run of
+// 2 N elements when they are interleaved.  Past the rotated part the rest of
+// the head is paired the same way, at angle zero.
+__device__ __forceinline__ void rope_runs(int j, int n, const RopeParams& p, int& e0, int& e1) {
+  if (p.interleaved) {
+    e0 = 2 * n * j;
+    e1 = e0 + n;
+    return;
+  }
+  const int half = p.rot / 2;
+  int i = n * j;
+  if (i < half) {
+    e0 = i;
+    e1 = i + half;
+  } else {
+    e0 = p.rot + (i - half);
+    e1 = e0 + (p.D - p.rot) / 2;
+  }
+}
+
+template <bool BF16, bool NORM>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p) {
+  extern __shared__ float2 s_cs[];               // [tokens][D / 2] cosine, sine
+  __shared__ int s_pos[kRopeThreads / 32];       // position, or -1: leave the row out
+  __shared__ long long s_dst[kRopeThreads / 32]; // first element of the row's head 0, or -1
+  constexpr int N = RopeVec<BF16>::N;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = p.D, half_d = D / 2;
+  const int lanes = half_d / N;                  // lane slots of a head
+  int width = 1;                                 // lanes of a group: a power of two
+  while (width < lanes) width *= 2;
+  const int j = threadIdx.x & (width - 1);
+  const int group = threadIdx.x / width, groups = kRopeThreads / width;
+  const int heads = p.qh + 2 * p.kvh;
+  const int r0 = blockIdx.x * p.tokens;
+  int e0, e1;
+  rope_runs(j < lanes ? j : 0, N, p, e0, e1);
+
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  // the group's first head goes in flight before the tokens are looked up
+  auto load = [&](int unit, uint4& a, uint4& b) {
+    const int t = unit / heads, h = unit - t * heads;
+    const int r = r0 + t;
+    if (t >= p.tokens || r >= p.pb.M || j >= lanes) return;
+    const bool isq = h < p.qh, isk = h < p.qh + p.kvh;
+    const void* src = isq ? p.Q : isk ? p.K : p.V;
+    const long long off = isq   ? (long long)r * p.ldq + (long long)h * D
+                          : isk ? (long long)r * p.ldk + (long long)(h - p.qh) * D
+                                : (long long)r * p.ldv + (long long)(h - p.qh - p.kvh) * D;
+    const char* base = reinterpret_cast<const char*>(src) + off * (BF16 ? 2 : 4);
+    a = *reinterpret_cast<const uint4*>(base + e0 * (BF16 ? 2 : 4));
+    b = *reinterpret_cast<const uint4*>(base + e1 * (BF16 ? 2 : 4));
+  };
+  uint4 a = make_uint4(0, 0, 0, 0), b = a;
+  load(group, a, b);
+
+  if (warp < p.tokens) {                         // one warp looks one token up
+    const int r = r0 + warp;
+    int pos = -1;
+    long long dst = -1;
+    if (r < p.pb.M) {
+      const int s = sequence_of(p.pb, r, lane);
+      if (s < p.pb.batch) {
+        const int c0 = __ldg(p.pb.cu_q + s), c1 = __ldg(p.pb.cu_q + s + 1);
+        const int len = __ldg(p.pb.kv_len + s);
+        pos = len - (c1 - r);
+        // c0 > r only in a table of rows that does not rise
+        if (pos < 0 || r < c0) {
+          pos = -1;
+        } else if (pos / p.pb.page_size >= p.pb.stride) {
+          if (lane == 0) record_device_error(DEV_ERR_INDEX);
+        } else {
+          const int page = __ldg(p.pb.table + (long long)s * p.pb.stride + pos / p.pb.page_size);
+          if (page < 0 || page >= p.pb.num_pages) {
+            if (lane == 0) record_device_error(DEV_ERR_INDEX);
+          } else {
+            dst = ((long long)page * p.kvh * p.pb.page_size + pos % p.pb.page_size) * D;
+          }
+        }
+      }
+    }
+    if (lane == 0) {
+      s_pos[warp] = pos;
+      s_dst[warp] = dst;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.tokens * half_d; i += kRopeThreads) {
+    const int t = i / half_d, f = i - t * half_d;
+    float2 cs = make_float2(1.0f, 0.0f);
+    if (f < p.rot / 2 && s_pos[t] >= 0) {
+      // turns = p * inv_freq / (2 pi); the nearest whole turn is dropped in fp64
+      double turns = (double)s_pos[t] * (double)__ldg(p.inv_freq + f) * 0.15915494309189533577;
+      turns -= rint(turns);
+      sincospif((float)(2.0 * turns), &cs.y, &cs.x);
+    }
+    s_cs[i] = cs;
+  }
+  __syncthreads();
+
+  // every lane of a warp makes the same number of trips: the norm's sums go
+  // through warp shuffles
+  const int units = p.tokens * heads, warp_group0 = (threadIdx.x & ~31) / width;
+  for (int unit = group, first = warp_group0; first < units; unit += groups, first += groups) {
+    uint4 na = make_uint4(0, 0, 0, 0), nb = na;
+    load(unit + groups, na, nb);
+    const int t = unit < units ? unit / heads : 0, h = unit - t * heads;
+    const bool isq = h < p.qh, isv = h >= p.qh + p.kvh;
+    const bool live = unit < units && j < lanes && s_pos[t] >= 0;
+    float x[2 * N];
+    RopeVec<BF16>::unpack(a, x);
+    RopeVec<BF16>::unpack(b, x + N);
+    float rr = 1.0f;
+    if (NORM) {
+      float sum = 0.0f;                          // idle lanes hold zeros
+#pragma unroll
+      for (int i = 0; i < 2 * N; ++i) sum = __fmaf_rn(x[i], x[i], sum);
+      for (int o = width / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      rr = 1.0f / sqrtf(sum / (float)D + p.eps);
+    }
+    if (!isv) {
+      if (NORM) {
+        const float* g = isq ? p.qg : p.kg;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          x[i] = x[i] * rr * (g ? __ldg(g + e0 + i) : 1.0f);
+          x[N + i] = x[N + i] * rr * (g ? __ldg(g + e1 + i) : 1.0f);
+        }
+      }
+      // pair index of the run's first pair
+      const float2* cs = s_cs + t * half_d + N * (j < lanes ? j : 0);
+      float y[2 * N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float2 w = cs[i];
+        const float u = p.interleaved ? x[2 * i] : x[i];
+        const float v = p.interleaved ? x[2 * i + 1] : x[N + i];
+        const float c = __fmaf_rn(u, w.x, -__fmul_rn(v, w.y));
+        const float d = __fmaf_rn(v, w.x, __fmul_rn(u, w.y));
+        if (p.interleaved) {
+          y[2 * i] = c;
+          y[2 * i + 1] = d;
+        } else {
+          y[i] = c;
+          y[N + i] = d;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * N; ++i) x[i] = y[i];
+    }
+    if (live) {
+      if (isq) {
+        const long long o = (long long)(r0 + t) * p.qh * D + (long long)h * D;
+        if (BF16) {
+          __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.Qo) + o;
+          store_bf16<N>(out + e0, x);
+          store_bf16<N>(out + e1, x + N);
+        } else {
+          float* out = reinterpret_cast<float*>(p.Qo) + o;
+          store_f32<N>(out + e0, x);
+          store_f32<N>(out + e1, x + N);
+        }
+      } else if (s_dst[t] >= 0) {
+        const int kh = isv ? h - p.qh - p.kvh : h - p.qh;
+        __nv_bfloat16* out =
+            (isv ? p.Vc : p.Kc) + s_dst[t] + (long long)kh * p.pb.page_size * D;
+        store_bf16<N>(out + e0, x);
+        store_bf16<N>(out + e1, x + N);
+      }
+    }
+    a = na;
+    b = nb;
+  }
+}
+
+}  // namespace bitnet
