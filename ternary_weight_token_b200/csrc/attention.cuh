@@ -92,7 +92,8 @@ struct PlanShared {
   SeqWork w;
 };
 
-// Inclusive scan over the first kAttnThreads threads' values (two at a time).
+// Inclusive scan over the first kAttnThreads threads' values (two at a time);
+// further threads of the CTA only keep the barriers.
 __device__ __forceinline__ void plan_scan(int& a, int& b, PlanShared& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int o = 1; o < 32; o *= 2) {
@@ -102,15 +103,16 @@ __device__ __forceinline__ void plan_scan(int& a, int& b, PlanShared& s) {
       b += y;
     }
   }
-  if (lane == 31) s.red[warp] = ((long long)b << 32) | (unsigned)a;
+  if (lane == 31 && warp < kAttnThreads / 32) s.red[warp] = ((long long)b << 32) | (unsigned)a;
   __syncthreads();
-  for (int i = 0; i < warp; ++i) {
+  for (int i = 0; i < warp && i < kAttnThreads / 32; ++i) {
     a += (int)(s.red[i] & 0xffffffffll);
     b += (int)(s.red[i] >> 32);
   }
 }
 
-// All kAttnThreads threads of the CTA.
+// All threads of the CTA, kAttnThreads at least (sequences of later threads
+// would start past the batch: they hold none).
 __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
   const int tid = threadIdx.x, B = p.pb.batch;
   const int per = (B + kAttnThreads - 1) / kAttnThreads;
@@ -124,7 +126,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
       u += (long long)w.tiles * w.units;
     }
     for (int o = 16; o > 0; o /= 2) u += __shfl_xor_sync(0xffffffffu, u, o);
-    if ((tid & 31) == 0) s.red[tid >> 5] = u;
+    if ((tid & 31) == 0 && tid < kAttnThreads) s.red[tid >> 5] = u;
     __syncthreads();
     u = 0;
     for (int i = 0; i < kAttnThreads / 32; ++i) u += s.red[i];
@@ -141,8 +143,10 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
   }
   const int mine = items, mine_s = slots;
   plan_scan(items, slots, s);
-  s.items[tid] = items - mine;
-  s.slots[tid] = slots - mine_s;
+  if (tid < kAttnThreads) {
+    s.items[tid] = items - mine;
+    s.slots[tid] = slots - mine_s;
+  }
   if (tid == kAttnThreads - 1) {
     s.items[kAttnThreads] = items;
     s.total = items;
@@ -161,10 +165,10 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
   __syncthreads();
 }
 
-// Sequence of item c, and its place there.  All kAttnThreads threads.
+// Sequence of item c, and its place there.  All threads of the CTA.
 __device__ __forceinline__ void find_item(const AttnParams& p, PlanShared& s, int c) {
   const int tid = threadIdx.x;
-  if (c >= s.items[tid] && c < s.items[tid + 1]) {
+  if (tid < kAttnThreads && c >= s.items[tid] && c < s.items[tid + 1]) {
     const int per = (p.pb.batch + kAttnThreads - 1) / kAttnThreads;
     const int b1 = min(p.pb.batch, (tid + 1) * per);
     int at = s.items[tid], slot = s.slots[tid];

@@ -1,0 +1,483 @@
+// attention_tc.cuh -- attention of chunks and prompts on the sm_100a tensor
+// cores (tcgen05.mma kind::f16, accumulators in tensor memory).
+//
+// The mathematics, the items and the splits are those of attention.cuh; an
+// item here is two row tiles of 128 (row t * G + g of a sequence is token t,
+// head g of the group) over blocks of 128 keys.  Per block and tile T
+//   S_T = Q_T K^T      A, B from shared memory, 128 x 128 fp32 into tensor memory
+//   P_T = 2^(S_T - m)  one thread per row, bf16, over S_T's columns
+//   O_T += P_T V       A from tensor memory, B = V as it lies (key rows, MN-major)
+// The two tiles alternate: while one is in the softmax the tensor core works on
+// the other.
+//
+// Running maximum: O_T is only rescaled when a row's maximum grows by more
+// than 2^8 (log2 units); until then the old reference stays, probabilities are
+// at most 2^8 and every sum is unchanged in exact arithmetic.
+//
+// Warp roles (384 threads, one CTA per SM):
+//   warps 0-3, 4-7  softmax of tile 0, 1: a thread owns a row (TMEM lane)
+//   warp 8          TMA producer: a ring of 128-key slots, K and V in turn,
+//                   one load per page piece and 64 columns
+//   warp 9          MMA issuer (one thread)
+//   warp 10         zeroes the value rows past the last key (whatever those
+//                   slots hold, 0 x NaN must not reach the sums)
+//   warp 11         tensor-memory allocator
+#pragma once
+
+#include "attention.cuh"
+#include "common.cuh"
+
+namespace bitnet {
+
+// D[tmem] (+)= A[smem] x B[smem]^T, kind::f16.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] x B[smem], kind::f16.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// kind::f16: D fp32, A and B bf16, A K-major, B K-major or MN-major.
+__host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// MN-major operand in the 128-byte swizzled layout: atoms of 64 elements (128
+// bytes) x 8 k; `mn_stride` bytes to the next 64 elements, 1024 to the next 8 k.
+__device__ __forceinline__ uint64_t make_sdesc_mn_sw128(uint32_t smem_addr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(mn_stride >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// registers -> 32 lanes x 16 columns of 32-bit TMEM.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+constexpr int kAttnTcThreads = 384;
+constexpr int kAttnTcTarget = 148;     // splits wanted: one per SM
+constexpr int kAttnTcKeys = 128;       // keys per block
+constexpr float kAttnTcLazy = 8.0f;    // growth of a row's maximum that rescales O
+
+template <int DP>
+struct AttnTcConfig {
+  static constexpr int RT = 256;
+  static constexpr int HALVES = DP / 64;                     // 64-column sub-tiles
+  static constexpr int SUB = 128 * 128;                      // bytes of one
+  static constexpr int TILE = HALVES * SUB;                  // Q tile, K or V block
+  static constexpr int SLOTS = DP == 128 ? 5 : 8;
+  static constexpr int OFF_KV = 2 * TILE;
+  static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
+  static constexpr int NUM_BARS = 2 * SLOTS + 10;
+  static constexpr int OFF_PLAN = OFF_BAR + NUM_BARS * 8 + 16;
+  static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanShared) + 1024;   // + alignment slack
+  static constexpr uint32_t S_COL = 0, O_COL = 256;          // + 128 T
+  static_assert(OFF_PLAN % 16 == 0 && SMEM <= 227 * 1024, "shared memory");
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kAttnTcThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, AttnParams p, int box_rows) {
+  using C = AttnTcConfig<DP>;
+  extern __shared__ uint8_t attn_tc_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(attn_tc_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* full = bars;                         // slot filled (TMA bytes)
+  uint64_t* empty = full + C::SLOTS;             // slot read (tcgen05.commit)
+  uint64_t* qfull = empty + C::SLOTS;            // both Q tiles written (8 warps)
+  uint64_t* sfull = qfull + 1;                   // [T] scores ready (commit)
+  uint64_t* pfull = sfull + 2;                   // [T] probabilities written (4 warps)
+  uint64_t* odone = pfull + 2;                   // [T] product with V done (commit)
+  uint64_t* vlast = odone + 2;                   // the block with the last key is here (issuer)
+  uint64_t* vfix = vlast + 1;                    // its rows past that key are zeroed (warp 10)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  PlanShared& plan = *reinterpret_cast<PlanShared*>(smem + C::OFF_PLAN);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = p.D;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::SLOTS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(qfull, 8);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sfull[t], 1);
+      mbar_init(&pfull[t], 4);
+      mbar_init(&odone[t], 1);
+    }
+    mbar_init(vlast, 1);
+    mbar_init(vfix, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 11) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const uint32_t tbase = *tmem_slot;
+  make_plan(p, plan);
+
+  uint32_t slot_it = 0;                          // ring position (producer, MMA, warp 10)
+  uint32_t items_done = 0, fixes = 0;
+  uint32_t blocks_done[2] = {0, 0};              // blocks of tile T so far
+
+  for (int c = blockIdx.x; c < plan.total; c += gridDim.x) {
+    find_item(p, plan, c);
+    const SeqWork w = plan.w;
+    const int splits = plan.splits, slot = plan.slot, b = plan.b;
+    if (b < 0) {
+      __syncthreads();
+      continue;
+    }
+    int tile, head, split;
+    item_place(p, w, plan.local, splits, tile, head, split);
+    const int rows = w.n * p.G, row0 = tile * C::RT;
+    const int nrows = min(C::RT, rows - row0);
+    const int past = w.len - w.n;
+    const int kv_end = max(0, past + (row0 + nrows - 1) / p.G + 1);
+    const int blocks = (kv_end + kAttnTcKeys - 1) / kAttnTcKeys;
+    const int blk0 = (int)((long long)blocks * split / splits);
+    const int blk1 = (int)((long long)blocks * (split + 1) / splits);
+    // blocks of each tile: tile 0 ends with the keys its last row sees
+    int cnt[2];
+    {
+      const int last0 = row0 + min(nrows, 128) - 1;
+      const int end0 = (max(0, past + last0 / p.G + 1) + kAttnTcKeys - 1) / kAttnTcKeys;
+      cnt[0] = max(0, min(blk1, end0) - blk0);
+      cnt[1] = nrows > 128 ? blk1 - blk0 : 0;
+    }
+    const int count = max(cnt[0], cnt[1]);
+    // the block that holds the last key needs its value rows past it zeroed
+    const int tail = kv_end - (blk0 + count - 1) * kAttnTcKeys;
+    const bool fix = count > 0 && tail < kAttnTcKeys;
+
+    if (warp == 8) {
+      // -------------------------------------------------------- producer
+      const int pieces = kAttnTcKeys / box_rows;             // loads per block and 64 columns
+      bool ok = true;
+      for (int i = 0; i < 2 * count; ++i, ++slot_it) {
+        const int key0 = (blk0 + (i >> 1)) * kAttnTcKeys;
+        // lane x < pieces: place of piece x (out of range: the load fills zeros)
+        const int key = key0 + lane * box_rows;
+        const bool live = lane < pieces && key < kv_end;
+        int page = -1;
+        if (live) {
+          page = __ldg(p.pb.table + (long long)b * p.pb.stride + key / p.pb.page_size);
+          if (page < 0 || page >= p.pb.num_pages) {
+            record_device_error(DEV_ERR_INDEX);
+            page = p.pb.num_pages;
+          }
+        }
+        const uint32_t st = slot_it % C::SLOTS, ph = (slot_it / C::SLOTS) & 1u;
+        if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t n_live = __popc(__ballot_sync(0xffffffffu, live));
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[st], n_live * (uint32_t)box_rows * 128u * C::HALVES);
+        __syncwarp();
+        if (live) {
+          uint8_t* dst = smem + C::OFF_KV + st * C::TILE + lane * box_rows * 128;
+#pragma unroll
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(dst + h * C::SUB, (i & 1) ? &tm_v : &tm_k, &full[st], 64 * h,
+                        key % p.pb.page_size, page * p.kvh + head);
+        }
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------ MMA issuer
+      if (lane == 0 && count > 0) {
+        constexpr uint32_t idesc_s = make_idesc_bf16(128, 128, false);
+        constexpr uint32_t idesc_o = make_idesc_bf16(128, DP, true);
+        const uint32_t qa = smem_u32(smem), kva = qa + C::OFF_KV;
+        auto scores = [&](int t, uint32_t ka) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint32_t o = (uint32_t)((k >> 2) * C::SUB + 32 * (k & 3));
+            mma_f16_ss(tbase + C::S_COL + 128u * t, make_sdesc_sw128(qa + t * C::TILE + o),
+                       make_sdesc_sw128(ka + o), idesc_s, k != 0);
+          }
+          tc_commit(&sfull[t]);
+        };
+        bool ok = mbar_wait(qfull, items_done & 1u, abort_flag);
+        uint32_t it = slot_it;
+        ok = ok && mbar_wait(&full[it % C::SLOTS], (it / C::SLOTS) & 1u, abort_flag);
+        if (ok) {
+          tc_fence_after();
+          for (int t = 0; t < 2; ++t)
+            if (cnt[t] > 0) scores(t, kva + (it % C::SLOTS) * C::TILE);
+          tc_commit(&empty[it % C::SLOTS]);
+          ++it;
+        }
+        for (int i = 0; ok && i < count; ++i) {
+          const uint32_t sv = it % C::SLOTS, sk = (it + 1) % C::SLOTS;
+          if (!mbar_wait(&full[sv], (it / C::SLOTS) & 1u, abort_flag)) break;
+          if (fix && i == count - 1) {
+            mbar_arrive(vlast);
+            if (!mbar_wait(vfix, fixes & 1u, abort_flag)) break;
+          }
+          const bool more = i + 1 < count;
+          bool kready = false;
+          for (int t = 0; t < 2; ++t) {
+            if (i >= cnt[t]) continue;
+            const uint32_t nth = blocks_done[t] + i;
+            if (!(ok = mbar_wait(&pfull[t], nth & 1u, abort_flag))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kAttnTcKeys / 16; ++k)
+              mma_f16_ts(tbase + C::O_COL + 128u * t, tbase + C::S_COL + 128u * t + 8u * k,
+                         make_sdesc_mn_sw128(kva + sv * C::TILE + 2048u * k, C::SUB), idesc_o,
+                         (i | k) != 0);
+            tc_commit(&odone[t]);
+            if (i + 1 < cnt[t]) {
+              if (!kready) {
+                if (!(ok = mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag))) break;
+                kready = true;
+              }
+              // the scores overwrite the probabilities the product reads
+              if (!(ok = mbar_wait(&odone[t], nth & 1u, abort_flag))) break;
+              tc_fence_after();
+              scores(t, kva + sk * C::TILE);
+            }
+          }
+          if (!ok) break;
+          tc_commit(&empty[sv]);
+          if (more) tc_commit(&empty[sk]);
+          it += 2;
+        }
+      }
+      __syncwarp();
+      slot_it += 2 * count;
+    } else if (warp == 10) {
+      // ------------------------------------------ value rows past the end
+      if (fix) {
+        const uint32_t it = slot_it + 2 * count - 1;
+        mbar_wait(vlast, fixes & 1u, abort_flag);
+        uint8_t* v = smem + C::OFF_KV + (it % C::SLOTS) * C::TILE;
+        for (int i = lane; i < (kAttnTcKeys - tail) * 8 * C::HALVES; i += 32) {
+          const int r = tail + (i >> 3) % (kAttnTcKeys - tail);
+          const int h = (i >> 3) / (kAttnTcKeys - tail);
+          *reinterpret_cast<uint4*>(v + h * C::SUB + r * 128 + (i & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vfix);
+      }
+      slot_it += 2 * count;
+    } else if (warp < 8) {
+      // --------------------------------------------------------- softmax
+      const int t = warp >> 2, r = threadIdx.x & 127;        // tile and row in it
+      const int row = 128 * t + r;                           // of the item
+      const bool live = row < nrows;
+      const int gr = row0 + (live ? row : 0);
+      const long long off =
+          ((long long)(w.c0 + gr / p.G) * p.qh + (long long)head * p.G + gr % p.G) * D;
+      {
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.Q) + off;
+        uint8_t* dst = smem + t * C::TILE + r * 128;
+#pragma unroll
+        for (int ch = 0; ch < DP / 8; ++ch) {
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (live && 8 * ch < D) u = *reinterpret_cast<const uint4*>(src + 8 * ch);
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::SUB + (((ch & 7) ^ (r & 7)) << 4)) = u;
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qfull);
+      }
+      const uint32_t lanes = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
+      const uint32_t scol = lanes + C::S_COL + 128u * t, ocol = lanes + C::O_COL + 128u * t;
+      const int lim = live ? past + gr / p.G + 1 : 0;        // keys this row sees
+      // keys that the warp's rows all see
+      const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
+      float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;             // m: reference, log2 units
+      bool ok = true;
+#pragma unroll 1
+      for (int i = 0; i < cnt[t]; ++i) {
+        if (!mbar_wait(&sfull[t], (blocks_done[t] + i) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(scol + 32u * q, s[q]);
+        tmem_ld_wait();
+        const int key0 = (blk0 + i) * kAttnTcKeys;
+        if (key0 + kAttnTcKeys > lim_warp) {
+          const int n = lim - key0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (32 * q + k >= n) s[q][k] = 0xff800000u;    // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+          for (int k = 1; k < 32; ++k) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][k]));
+        }
+        const float mnew =
+            fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        if (i == 0) {
+          m = mnew;
+        } else {
+          const bool grow = mnew > m + kAttnTcLazy || (m == -INFINITY && mnew != -INFINITY);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float next = grow ? mnew : m;
+            const float f = grow ? ex2(m - mnew) : 1.0f;
+            l0 *= f;
+            l1 *= f;
+            m = next;
+            // the product of the last block is done: its completion precedes
+            // that of the scores just read
+#pragma unroll 1
+            for (int d = 0; d < DP; d += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(ocol + d, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st_32x32b_x32(ocol + d, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float base = m == -INFINITY ? 0.0f : -m;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t ph[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float x = ex2(__fmaf_rn(__uint_as_float(s[q][2 * k]), p.scale_log2, base));
+            const float y = ex2(__fmaf_rn(__uint_as_float(s[q][2 * k + 1]), p.scale_log2, base));
+            l0 += x;
+            l1 += y;
+            ph[k] = pack_bf16x2(x, y);
+          }
+          tmem_st_32x32b_x16(scol + 16u * q, ph);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[t]);
+      }
+      // ---- the rows' sums
+      const float l = l0 + l1;
+      if (ok && cnt[t] > 0)
+        ok = mbar_wait(&odone[t], (blocks_done[t] + cnt[t] - 1) & 1u, abort_flag);
+      tc_fence_after();
+      if (ok && 128 * t < nrows) {
+        float* part = slot >= 0 ? p.part + (long long)slot * C::RT * (D + 2) : nullptr;
+        const float inv = slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+        if (slot >= 0 && live) {
+          part[row] = m;
+          part[C::RT + row] = l;
+        }
+#pragma unroll 1
+        for (int d = 0; d < DP; d += 32) {
+          uint32_t o[32];
+          if (cnt[t] > 0) {
+            tmem_ld_32x32b_x32(ocol + d, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[k + e]) * inv;
+            if (live && d + k < D) {
+              if (slot >= 0)
+                store_f32<8>(part + 2 * C::RT + (long long)row * D + d + k, x);
+              else
+                store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(p.O) + off + d + k, x);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+    }
+    blocks_done[0] += cnt[0];
+    blocks_done[1] += cnt[1];
+    ++items_done;
+    if (fix) ++fixes;
+    __syncthreads();                             // plan, Q tiles and tensor memory are free
+    tc_fence_after();
+    if (*abort_flag) break;
+  }
+
+  // Never leave tensor-core work or bulk copies in flight (an abort can).
+  if (*abort_flag) {
+    if (warp == 9 && lane == 0) {
+      tc_commit(&odone[0]);
+      mbar_wait(&odone[0], 0, nullptr, 100000000ull);
+      mbar_wait(&odone[0], 1, nullptr, 100000000ull);
+    }
+    if (warp == 8 && lane == 0) {
+      const uint32_t last = slot_it < (uint32_t)C::SLOTS ? slot_it : (uint32_t)C::SLOTS;
+      for (uint32_t i = 0; i < last; ++i) {
+        const uint32_t j = slot_it - 1 - i;
+        mbar_wait(&full[j % C::SLOTS], (j / C::SLOTS) & 1u, nullptr, 100000000ull);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 11) tmem_dealloc(tbase, 512);
+}
+
+}  // namespace bitnet

@@ -22,6 +22,7 @@
 
 #include "../../include/bitnet.h"
 #include "attention.cuh"
+#include "attention_tc.cuh"
 #include "common.cuh"
 #include "ffn_decode.cuh"
 #include "gemm_tc.cuh"
@@ -869,21 +870,59 @@ int validate_paged(int dtype, int M, int q_heads, int kv_heads, int head_dim, in
 
 // Row tile and split target of an attention call (pure host logic).
 struct AttnShape {
+  bool tc;                             // tensor-core kernel
   int RT, unit, min_units, target;
 };
 
-AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim) {
+AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, bool f32,
+                     float scale) {
   const int G = q_heads / kv_heads;
-  AttnShape sh;
-  // tiles of 16 rows while a sequence has that many on average, else of 64;
-  // heads wider than 128 do not leave the registers for 64
-  sh.RT = (long long)M * G <= 16ll * batch || head_dim > 128 ? 16 : 64;
-  sh.unit = kAttnTile;
-  sh.min_units = 4;
-  sh.target = kAttnTarget;
+  AttnShape sh = {};
+  // Up to 16 rows per sequence on average: tiles of 16, the keys of a block
+  // shared out to four warps.  Above, the tensor-core kernel's pairs of
+  // 128-row tiles for bf16; its softmax wants a positive scale.  What is left
+  // takes tiles of 64, heads wider than 128 (no registers for 64) of 16.
+  const bool few = (long long)M * G <= 16ll * batch;
+  sh.tc = !few && !f32 && head_dim <= 128 && scale > 0.0f;
+  if (sh.tc) {
+    sh.RT = 256;
+    sh.unit = kAttnTcKeys;
+    sh.min_units = 2;
+    sh.target = kAttnTcTarget;
+  } else {
+    sh.RT = few || head_dim > 128 ? 16 : 64;
+    sh.unit = kAttnTile;
+    sh.min_units = 4;
+    sh.target = kAttnTarget;
+  }
   // enough items without splitting
-  if ((long long)M * G / sh.RT * kv_heads >= 2 * kAttnTarget) sh.target = 0;
+  if ((long long)M * G / sh.RT * kv_heads >= 2 * sh.target) sh.target = 0;
   return sh;
+}
+
+template <int DP>
+int launch_attn_tc(const AttnParams& p, int sms, cudaStream_t st) {
+  using C = AttnTcConfig<DP>;
+  // page pieces that neither a page nor a block of keys cuts
+  int box = 16;
+  while (box < kAttnTcKeys && p.pb.page_size % (2 * box) == 0) box *= 2;
+  CUtensorMap mk, mv;
+  const cuuint64_t row = (cuuint64_t)p.D * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.pb.page_size,
+                              (cuuint64_t)p.pb.num_pages * p.kvh};
+  const cuuint64_t strides[2] = {row, row * p.pb.page_size};
+  const cuuint32_t bx[3] = {64, (cuuint32_t)box, 1};
+  if (int rc = encode_map(mk, p.Kc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, bx,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+    return rc;
+  if (int rc = encode_map(mv, p.Vc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dims, strides, bx,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+    return rc;
+  auto kern = attn_tc_kernel<DP>;
+  if (int rc = set_smem_attr((const void*)kern, C::SMEM)) return rc;
+  const long long items = ((long long)p.pb.M * p.G / C::RT + p.pb.batch) * p.kvh + p.target;
+  const int grid = (int)std::min<long long>(items, sms);
+  return launch_pdl(kern, dim3(grid), dim3(kAttnTcThreads), C::SMEM, st, mk, mv, p, box);
 }
 
 template <int DP, int WR, bool F32>
@@ -1538,6 +1577,8 @@ size_t bitnet_attention_workspace_size(int M, int batch, int q_heads, int kv_hea
       head_dim < 1 || head_dim > kRopeMaxDim)
     return 0;
   // the largest that a call of at most M rows and `batch` sequences takes
+  // (the split slots of tiles of 64 and of 256 rows take the same room)
+  static_assert(kAttnTarget * 64 >= kAttnTcTarget * 256, "split slots");
   const int rt = (long long)M * (q_heads / kv_heads) <= 16 || head_dim > 128 ? 16 : 64;
   return align256(((size_t)batch + kAttnPlanHead) * 4) +
          (size_t)2 * kAttnTarget * rt * (head_dim + 2) * 4;
@@ -1570,7 +1611,8 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   if (!aligned16(workspace)) return fail(BITNET_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   DeviceInfo di;
   if (int rc = device_info(di)) return rc;
-  const AttnShape sh = attn_shape(M, batch, q_heads, kv_heads, head_dim);
+  const bool f32 = dtype == BITNET_F32;
+  const AttnShape sh = attn_shape(M, batch, q_heads, kv_heads, head_dim, f32, scale);
   AttnParams p = {};
   p.pb = {cu_q, kv_len, block_table, batch, table_stride, num_pages, page_size, M};
   p.Q = Q; p.O = O;
@@ -1585,9 +1627,10 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
                                     align256(((size_t)batch + kAttnPlanHead) * 4));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool f32 = dtype == BITNET_F32;
   int rc;
-  if (sh.RT == 16)
+  if (sh.tc)
+    rc = head_dim <= 64 ? launch_attn_tc<64>(p, di.sms, st) : launch_attn_tc<128>(p, di.sms, st);
+  else if (sh.RT == 16)
     rc = f32 ? launch_attn_dim<1, true>(p, di.sms, st) : launch_attn_dim<1, false>(p, di.sms, st);
   else
     rc = f32 ? launch_attn_dim<4, true>(p, di.sms, st) : launch_attn_dim<4, false>(p, di.sms, st);
