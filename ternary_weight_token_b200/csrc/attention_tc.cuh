@@ -89,6 +89,26 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
+// Two fp32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 constexpr int kAttnTcThreads = 384;
 constexpr int kAttnTcTarget = 148;     // splits wanted: one per SM
 constexpr int kAttnTcKeys = 128;       // keys per block
@@ -167,158 +187,69 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
   uint32_t items_done = 0, fixes = 0;
   uint32_t blocks_done[2] = {0, 0};              // blocks of tile T so far
 
-  for (int c = blockIdx.x; c < plan.total; c += gridDim.x) {
-    find_item(p, plan, c);
-    const SeqWork w = plan.w;
-    const int splits = plan.splits, slot = plan.slot, b = plan.b;
-    if (b < 0) {
-      __syncthreads();
-      continue;
+  // Every role walks the same items; `role` does its part of one.
+  struct Item {
+    SeqWork w;
+    int b, head, slot, row0, nrows, past, kv_end, blk0, count, tail;
+    int cnt[2];                                  // blocks of each tile
+    bool fix;
+  };
+  auto walk = [&](auto&& role) {
+    for (int wave = 0;; ++wave) {
+      // items come longest first: every other wave runs the other way round,
+      // so that a CTA's share evens out
+      const int at = (wave & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+      const long long c = (long long)wave * gridDim.x + at;
+      if ((long long)wave * gridDim.x >= plan.total) break;
+      if (c >= plan.total) continue;
+      find_item(p, plan, (int)c);
+      if (plan.b >= 0) {
+        Item job;
+        job.w = plan.w;
+        job.b = plan.b;
+        job.slot = plan.slot;
+        int tile, split;
+        item_place(p, job.w, plan.local, plan.splits, tile, job.head, split);
+        job.row0 = tile * C::RT;
+        job.nrows = min(C::RT, job.w.n * p.G - job.row0);
+        job.past = job.w.len - job.w.n;
+        job.kv_end = max(0, job.past + (job.row0 + job.nrows - 1) / p.G + 1);
+        const int blocks = (job.kv_end + kAttnTcKeys - 1) / kAttnTcKeys;
+        job.blk0 = (int)((long long)blocks * split / plan.splits);
+        const int blk1 = (int)((long long)blocks * (split + 1) / plan.splits);
+        // tile 0 ends with the keys its last row sees
+        const int last0 = job.row0 + min(job.nrows, 128) - 1;
+        const int end0 = (max(0, job.past + last0 / p.G + 1) + kAttnTcKeys - 1) / kAttnTcKeys;
+        job.cnt[0] = max(0, min(blk1, end0) - job.blk0);
+        job.cnt[1] = job.nrows > 128 ? blk1 - job.blk0 : 0;
+        job.count = max(job.cnt[0], job.cnt[1]);
+        // the block that holds the last key needs its value rows past it zeroed
+        job.tail = job.kv_end - (job.blk0 + job.count - 1) * kAttnTcKeys;
+        job.fix = job.count > 0 && job.tail < kAttnTcKeys;
+        role(job);
+        slot_it += 2 * job.count;
+        blocks_done[0] += job.cnt[0];
+        blocks_done[1] += job.cnt[1];
+        ++items_done;
+        if (job.fix) ++fixes;
+      }
+      tc_fence_before();
+      __syncthreads();                           // plan, Q tiles and tensor memory are free
+      tc_fence_after();
+      if (*abort_flag) break;
     }
-    int tile, head, split;
-    item_place(p, w, plan.local, splits, tile, head, split);
-    const int rows = w.n * p.G, row0 = tile * C::RT;
-    const int nrows = min(C::RT, rows - row0);
-    const int past = w.len - w.n;
-    const int kv_end = max(0, past + (row0 + nrows - 1) / p.G + 1);
-    const int blocks = (kv_end + kAttnTcKeys - 1) / kAttnTcKeys;
-    const int blk0 = (int)((long long)blocks * split / splits);
-    const int blk1 = (int)((long long)blocks * (split + 1) / splits);
-    // blocks of each tile: tile 0 ends with the keys its last row sees
-    int cnt[2];
-    {
-      const int last0 = row0 + min(nrows, 128) - 1;
-      const int end0 = (max(0, past + last0 / p.G + 1) + kAttnTcKeys - 1) / kAttnTcKeys;
-      cnt[0] = max(0, min(blk1, end0) - blk0);
-      cnt[1] = nrows > 128 ? blk1 - blk0 : 0;
-    }
-    const int count = max(cnt[0], cnt[1]);
-    // the block that holds the last key needs its value rows past it zeroed
-    const int tail = kv_end - (blk0 + count - 1) * kAttnTcKeys;
-    const bool fix = count > 0 && tail < kAttnTcKeys;
+  };
 
-    if (warp == 8) {
-      // -------------------------------------------------------- producer
-      const int pieces = kAttnTcKeys / box_rows;             // loads per block and 64 columns
-      bool ok = true;
-      for (int i = 0; i < 2 * count; ++i, ++slot_it) {
-        const int key0 = (blk0 + (i >> 1)) * kAttnTcKeys;
-        // lane x < pieces: place of piece x (out of range: the load fills zeros)
-        const int key = key0 + lane * box_rows;
-        const bool live = lane < pieces && key < kv_end;
-        int page = -1;
-        if (live) {
-          page = __ldg(p.pb.table + (long long)b * p.pb.stride + key / p.pb.page_size);
-          if (page < 0 || page >= p.pb.num_pages) {
-            record_device_error(DEV_ERR_INDEX);
-            page = p.pb.num_pages;
-          }
-        }
-        const uint32_t st = slot_it % C::SLOTS, ph = (slot_it / C::SLOTS) & 1u;
-        if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t n_live = __popc(__ballot_sync(0xffffffffu, live));
-        if (lane == 0)
-          mbar_arrive_expect_tx(&full[st], n_live * (uint32_t)box_rows * 128u * C::HALVES);
-        __syncwarp();
-        if (live) {
-          uint8_t* dst = smem + C::OFF_KV + st * C::TILE + lane * box_rows * 128;
-#pragma unroll
-          for (int h = 0; h < C::HALVES; ++h)
-            tma_load_3d(dst + h * C::SUB, (i & 1) ? &tm_v : &tm_k, &full[st], 64 * h,
-                        key % p.pb.page_size, page * p.kvh + head);
-        }
-      }
-    } else if (warp == 9) {
-      // ------------------------------------------------------ MMA issuer
-      if (lane == 0 && count > 0) {
-        constexpr uint32_t idesc_s = make_idesc_bf16(128, 128, false);
-        constexpr uint32_t idesc_o = make_idesc_bf16(128, DP, true);
-        const uint32_t qa = smem_u32(smem), kva = qa + C::OFF_KV;
-        auto scores = [&](int t, uint32_t ka) {
-#pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const uint32_t o = (uint32_t)((k >> 2) * C::SUB + 32 * (k & 3));
-            mma_f16_ss(tbase + C::S_COL + 128u * t, make_sdesc_sw128(qa + t * C::TILE + o),
-                       make_sdesc_sw128(ka + o), idesc_s, k != 0);
-          }
-          tc_commit(&sfull[t]);
-        };
-        bool ok = mbar_wait(qfull, items_done & 1u, abort_flag);
-        uint32_t it = slot_it;
-        ok = ok && mbar_wait(&full[it % C::SLOTS], (it / C::SLOTS) & 1u, abort_flag);
-        if (ok) {
-          tc_fence_after();
-          for (int t = 0; t < 2; ++t)
-            if (cnt[t] > 0) scores(t, kva + (it % C::SLOTS) * C::TILE);
-          tc_commit(&empty[it % C::SLOTS]);
-          ++it;
-        }
-        for (int i = 0; ok && i < count; ++i) {
-          const uint32_t sv = it % C::SLOTS, sk = (it + 1) % C::SLOTS;
-          if (!mbar_wait(&full[sv], (it / C::SLOTS) & 1u, abort_flag)) break;
-          if (fix && i == count - 1) {
-            mbar_arrive(vlast);
-            if (!mbar_wait(vfix, fixes & 1u, abort_flag)) break;
-          }
-          const bool more = i + 1 < count;
-          bool kready = false;
-          for (int t = 0; t < 2; ++t) {
-            if (i >= cnt[t]) continue;
-            const uint32_t nth = blocks_done[t] + i;
-            if (!(ok = mbar_wait(&pfull[t], nth & 1u, abort_flag))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kAttnTcKeys / 16; ++k)
-              mma_f16_ts(tbase + C::O_COL + 128u * t, tbase + C::S_COL + 128u * t + 8u * k,
-                         make_sdesc_mn_sw128(kva + sv * C::TILE + 2048u * k, C::SUB), idesc_o,
-                         (i | k) != 0);
-            tc_commit(&odone[t]);
-            if (i + 1 < cnt[t]) {
-              if (!kready) {
-                if (!(ok = mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag))) break;
-                kready = true;
-              }
-              // the scores overwrite the probabilities the product reads
-              if (!(ok = mbar_wait(&odone[t], nth & 1u, abort_flag))) break;
-              tc_fence_after();
-              scores(t, kva + sk * C::TILE);
-            }
-          }
-          if (!ok) break;
-          tc_commit(&empty[sv]);
-          if (more) tc_commit(&empty[sk]);
-          it += 2;
-        }
-      }
-      __syncwarp();
-      slot_it += 2 * count;
-    } else if (warp == 10) {
-      // ------------------------------------------ value rows past the end
-      if (fix) {
-        const uint32_t it = slot_it + 2 * count - 1;
-        mbar_wait(vlast, fixes & 1u, abort_flag);
-        uint8_t* v = smem + C::OFF_KV + (it % C::SLOTS) * C::TILE;
-        for (int i = lane; i < (kAttnTcKeys - tail) * 8 * C::HALVES; i += 32) {
-          const int r = tail + (i >> 3) % (kAttnTcKeys - tail);
-          const int h = (i >> 3) / (kAttnTcKeys - tail);
-          *reinterpret_cast<uint4*>(v + h * C::SUB + r * 128 + (i & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vfix);
-      }
-      slot_it += 2 * count;
-    } else if (warp < 8) {
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    walk([&](const Item& job) {
       // --------------------------------------------------------- softmax
       const int t = warp >> 2, r = threadIdx.x & 127;        // tile and row in it
       const int row = 128 * t + r;                           // of the item
-      const bool live = row < nrows;
-      const int gr = row0 + (live ? row : 0);
+      const bool live = row < job.nrows;
+      const int gr = job.row0 + (live ? row : 0);
       const long long off =
-          ((long long)(w.c0 + gr / p.G) * p.qh + (long long)head * p.G + gr % p.G) * D;
+          ((long long)(job.w.c0 + gr / p.G) * p.qh + (long long)job.head * p.G + gr % p.G) * D;
       {
         const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.Q) + off;
         uint8_t* dst = smem + t * C::TILE + r * 128;
@@ -334,13 +265,14 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       }
       const uint32_t lanes = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
       const uint32_t scol = lanes + C::S_COL + 128u * t, ocol = lanes + C::O_COL + 128u * t;
-      const int lim = live ? past + gr / p.G + 1 : 0;        // keys this row sees
+      const int lim = live ? job.past + gr / p.G + 1 : 0;        // keys this row sees
       // keys that the warp's rows all see
       const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
-      float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;             // m: reference, log2 units
+      float m = -INFINITY;                                   // reference, log2 units
+      uint64_t l2 = 0;                                       // two partial sums
       bool ok = true;
 #pragma unroll 1
-      for (int i = 0; i < cnt[t]; ++i) {
+      for (int i = 0; i < job.cnt[t]; ++i) {
         if (!mbar_wait(&sfull[t], (blocks_done[t] + i) & 1u, abort_flag)) {
           ok = false;
           break;
@@ -350,7 +282,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(scol + 32u * q, s[q]);
         tmem_ld_wait();
-        const int key0 = (blk0 + i) * kAttnTcKeys;
+        const int key0 = (job.blk0 + i) * kAttnTcKeys;
         if (key0 + kAttnTcKeys > lim_warp) {
           const int n = lim - key0;
 #pragma unroll
@@ -375,8 +307,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
           if (__any_sync(0xffffffffu, grow)) {
             const float next = grow ? mnew : m;
             const float f = grow ? ex2(m - mnew) : 1.0f;
-            l0 *= f;
-            l1 *= f;
+            l2 = fma_f32x2(l2, pack_f32x2(f, f), 0);
             m = next;
             // the product of the last block is done: its completion precedes
             // that of the scores just read
@@ -393,15 +324,20 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
           }
         }
         const float base = m == -INFINITY ? 0.0f : -m;
+        const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+        const uint64_t base2 = pack_f32x2(base, base);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t ph[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float x = ex2(__fmaf_rn(__uint_as_float(s[q][2 * k]), p.scale_log2, base));
-            const float y = ex2(__fmaf_rn(__uint_as_float(s[q][2 * k + 1]), p.scale_log2, base));
-            l0 += x;
-            l1 += y;
+            float x, y;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[q][2 * k]),
+                                              __uint_as_float(s[q][2 * k + 1])), scale2, base2),
+                         x, y);
+            x = ex2(x);
+            y = ex2(y);
+            l2 = add_f32x2(l2, pack_f32x2(x, y));
             ph[k] = pack_bf16x2(x, y);
           }
           tmem_st_32x32b_x16(scol + 16u * q, ph);
@@ -412,21 +348,23 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         if (lane == 0) mbar_arrive(&pfull[t]);
       }
       // ---- the rows' sums
-      const float l = l0 + l1;
-      if (ok && cnt[t] > 0)
-        ok = mbar_wait(&odone[t], (blocks_done[t] + cnt[t] - 1) & 1u, abort_flag);
+      float l, lb;
+      unpack_f32x2(l2, l, lb);
+      l += lb;
+      if (ok && job.cnt[t] > 0)
+        ok = mbar_wait(&odone[t], (blocks_done[t] + job.cnt[t] - 1) & 1u, abort_flag);
       tc_fence_after();
-      if (ok && 128 * t < nrows) {
-        float* part = slot >= 0 ? p.part + (long long)slot * C::RT * (D + 2) : nullptr;
-        const float inv = slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
-        if (slot >= 0 && live) {
+      if (ok && 128 * t < job.nrows) {
+        float* part = job.slot >= 0 ? p.part + (long long)job.slot * C::RT * (D + 2) : nullptr;
+        const float inv = job.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+        if (job.slot >= 0 && live) {
           part[row] = m;
           part[C::RT + row] = l;
         }
 #pragma unroll 1
         for (int d = 0; d < DP; d += 32) {
           uint32_t o[32];
-          if (cnt[t] > 0) {
+          if (job.cnt[t] > 0) {
             tmem_ld_32x32b_x32(ocol + d, o);
             tmem_ld_wait();
           } else {
@@ -439,7 +377,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[k + e]) * inv;
             if (live && d + k < D) {
-              if (slot >= 0)
+              if (job.slot >= 0)
                 store_f32<8>(part + 2 * C::RT + (long long)row * D + d + k, x);
               else
                 store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(p.O) + off + d + k, x);
@@ -449,14 +387,131 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         }
       }
       tc_fence_before();
+    });
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 8) {
+      walk([&](const Item& job) {
+      // -------------------------------------------------------- producer
+      const int pieces = kAttnTcKeys / box_rows;             // loads per block and 64 columns
+      bool ok = true;
+      for (int i = 0; i < 2 * job.count; ++i) {
+        const uint32_t it = slot_it + i;
+        const int key0 = (job.blk0 + (i >> 1)) * kAttnTcKeys;
+        // lane x < pieces: place of piece x (out of range: the load fills zeros)
+        const int key = key0 + lane * box_rows;
+        const bool live = lane < pieces && key < job.kv_end;
+        int page = -1;
+        if (live) {
+          page = __ldg(p.pb.table + (long long)job.b * p.pb.stride + key / p.pb.page_size);
+          if (page < 0 || page >= p.pb.num_pages) {
+            record_device_error(DEV_ERR_INDEX);
+            page = p.pb.num_pages;
+          }
+        }
+        const uint32_t st = it % C::SLOTS, ph = (it / C::SLOTS) & 1u;
+        if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t n_live = __popc(__ballot_sync(0xffffffffu, live));
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[st], n_live * (uint32_t)box_rows * 128u * C::HALVES);
+        __syncwarp();
+        if (live) {
+          uint8_t* dst = smem + C::OFF_KV + st * C::TILE + lane * box_rows * 128;
+#pragma unroll
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(dst + h * C::SUB, (i & 1) ? &tm_v : &tm_k, &full[st], 64 * h,
+                        key % p.pb.page_size, page * p.kvh + job.head);
+        }
+      }
+      });
+    } else if (warp == 9) {
+      walk([&](const Item& job) {
+      // ------------------------------------------------------ MMA issuer
+      if (lane == 0 && job.count > 0) {
+        constexpr uint32_t idesc_s = make_idesc_bf16(128, 128, false);
+        constexpr uint32_t idesc_o = make_idesc_bf16(128, DP, true);
+        const uint32_t qa = smem_u32(smem), kva = qa + C::OFF_KV;
+        auto scores = [&](int t, uint32_t ka) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint32_t o = (uint32_t)((k >> 2) * C::SUB + 32 * (k & 3));
+            mma_f16_ss(tbase + C::S_COL + 128u * t, make_sdesc_sw128(qa + t * C::TILE + o),
+                       make_sdesc_sw128(ka + o), idesc_s, k != 0);
+          }
+          tc_commit(&sfull[t]);
+        };
+        bool ok = mbar_wait(qfull, items_done & 1u, abort_flag);
+        uint32_t it = slot_it;
+        ok = ok && mbar_wait(&full[it % C::SLOTS], (it / C::SLOTS) & 1u, abort_flag);
+        if (ok) {
+          tc_fence_after();
+          for (int t = 0; t < 2; ++t)
+            if (job.cnt[t] > 0) scores(t, kva + (it % C::SLOTS) * C::TILE);
+          tc_commit(&empty[it % C::SLOTS]);
+          ++it;
+        }
+        for (int i = 0; ok && i < job.count; ++i) {
+          const uint32_t sv = it % C::SLOTS, sk = (it + 1) % C::SLOTS;
+          if (!mbar_wait(&full[sv], (it / C::SLOTS) & 1u, abort_flag)) break;
+          if (job.fix && i == job.count - 1) {
+            mbar_arrive(vlast);
+            if (!mbar_wait(vfix, fixes & 1u, abort_flag)) break;
+          }
+          const bool more = i + 1 < job.count;
+          bool kready = false;
+          for (int t = 0; t < 2; ++t) {
+            if (i >= job.cnt[t]) continue;
+            const uint32_t nth = blocks_done[t] + i;
+            if (!(ok = mbar_wait(&pfull[t], nth & 1u, abort_flag))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kAttnTcKeys / 16; ++k)
+              mma_f16_ts(tbase + C::O_COL + 128u * t, tbase + C::S_COL + 128u * t + 8u * k,
+                         make_sdesc_mn_sw128(kva + sv * C::TILE + 2048u * k, C::SUB), idesc_o,
+                         (i | k) != 0);
+            tc_commit(&odone[t]);
+            if (i + 1 < job.cnt[t]) {
+              if (!kready) {
+                if (!(ok = mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag))) break;
+                kready = true;
+              }
+              // the scores overwrite the probabilities the product reads
+              if (!(ok = mbar_wait(&odone[t], nth & 1u, abort_flag))) break;
+              tc_fence_after();
+              scores(t, kva + sk * C::TILE);
+            }
+          }
+          if (!ok) break;
+          tc_commit(&empty[sv]);
+          if (more) tc_commit(&empty[sk]);
+          it += 2;
+        }
+      }
+      __syncwarp();
+      });
+    } else if (warp == 10) {
+      walk([&](const Item& job) {
+      // ------------------------------------------ value rows past the end
+      if (job.fix) {
+        const uint32_t it = slot_it + 2 * job.count - 1;
+        mbar_wait(vlast, fixes & 1u, abort_flag);
+        uint8_t* v = smem + C::OFF_KV + (it % C::SLOTS) * C::TILE;
+        for (int i = lane; i < (kAttnTcKeys - job.tail) * 8 * C::HALVES; i += 32) {
+          const int r = job.tail + (i >> 3) % (kAttnTcKeys - job.tail);
+          const int h = (i >> 3) / (kAttnTcKeys - job.tail);
+          *reinterpret_cast<uint4*>(v + h * C::SUB + r * 128 + (i & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vfix);
+      }
+      });
+    } else {
+      walk([&](const Item&) {});
     }
-    blocks_done[0] += cnt[0];
-    blocks_done[1] += cnt[1];
-    ++items_done;
-    if (fix) ++fixes;
-    __syncthreads();                             // plan, Q tiles and tensor memory are free
-    tc_fence_after();
-    if (*abort_flag) break;
   }
 
   // Never leave tensor-core work or bulk copies in flight (an abort can).
