@@ -165,30 +165,40 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
   __syncthreads();
 }
 
-// Sequence of item c, and its place there.  All threads of the CTA.
-__device__ __forceinline__ void find_item(const AttnParams& p, PlanShared& s, int c) {
+// Calls take(b, work, local, splits, slot) on the one thread whose sequences
+// hold item c (on none if the lengths changed under the call).
+template <class F>
+__device__ __forceinline__ void find_item_as(const AttnParams& p, const PlanShared& s, int c,
+                                             F&& take) {
   const int tid = threadIdx.x;
-  if (tid < kAttnThreads && c >= s.items[tid] && c < s.items[tid + 1]) {
-    const int per = (p.pb.batch + kAttnThreads - 1) / kAttnThreads;
-    const int b1 = min(p.pb.batch, (tid + 1) * per);
-    int at = s.items[tid], slot = s.slots[tid];
-    s.b = -1;                          // kept only if the lengths changed under the call
-    for (int b = tid * per; b < b1; ++b) {
-      const SeqWork w = seq_work(p, b, false);
-      const int sp = splits_of(w.units, s.chunk);
-      const int k = w.tiles * p.kvh * sp;
-      if (c < at + k) {
-        s.b = b;
-        s.w = w;
-        s.local = c - at;
-        s.splits = sp;
-        s.slot = sp > 1 ? slot + (c - at) : -1;
-        break;
-      }
-      at += k;
-      if (sp > 1) slot += k;
+  if (tid >= kAttnThreads || c < s.items[tid] || c >= s.items[tid + 1]) return;
+  const int per = (p.pb.batch + kAttnThreads - 1) / kAttnThreads;
+  const int b1 = min(p.pb.batch, (tid + 1) * per);
+  int at = s.items[tid], slot = s.slots[tid];
+  for (int b = tid * per; b < b1; ++b) {
+    const SeqWork w = seq_work(p, b, false);
+    const int sp = splits_of(w.units, s.chunk);
+    const int k = w.tiles * p.kvh * sp;
+    if (c < at + k) {
+      take(b, w, c - at, sp, sp > 1 ? slot + (c - at) : -1);
+      return;
     }
+    at += k;
+    if (sp > 1) slot += k;
   }
+}
+
+// Sequence of item c, and its place there, in the plan.  All threads of the CTA.
+__device__ __forceinline__ void find_item(const AttnParams& p, PlanShared& s, int c) {
+  if (threadIdx.x == 0) s.b = -1;
+  __syncthreads();
+  find_item_as(p, s, c, [&](int b, const SeqWork& w, int local, int splits, int slot) {
+    s.b = b;
+    s.w = w;
+    s.local = local;
+    s.splits = splits;
+    s.slot = slot;
+  });
   __syncthreads();
 }
 

@@ -18,11 +18,12 @@
 //   warps 0-3, 4-7  softmax of tile 0, 1: a thread owns a row (TMEM lane)
 //   warp 8          TMA producer: a ring of 128-key slots, K and V in turn,
 //                   one load per page piece and 64 columns
-//   warp 9          MMA issuer (one thread)
+//   warps 9, 11     MMA issuers of tile 0, 1 (11 also holds the tensor memory)
 //   warp 10         zeroes the value rows past the last key (whatever those
 //                   slots hold, 0 x NaN must not reach the sums)
-//   warp 11         tensor-memory allocator
 #pragma once
+
+#include <type_traits>
 
 #include "attention.cuh"
 #include "common.cuh"
@@ -69,6 +70,17 @@ __device__ __forceinline__ uint64_t make_sdesc_mn_sw128(uint32_t smem_addr, uint
   return d;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
+
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
                                             int x, int y, int z) {
   asm volatile(
@@ -109,10 +121,47 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 2^x of two finite values on the fp32 pipe instead of the exponential unit
+// (16 results per cycle and SM, which bounds the softmax): n = rint(x), a cubic
+// in f = x - n on [-1/2, 1/2] (minimax in the relative error by
+// Remez exchange, 7.5e-5: a fiftieth of the bf16 rounding that follows), n added to the exponent.
+__device__ __forceinline__ void ex2_poly2(uint64_t z, float& x, float& y) {
+  constexpr float kRound = 12582912.0f;          // 1.5 * 2^23: the sum's low bits are n
+  constexpr float c0 = 0.99992807f, c1 = 0.69326099f, c2 = 0.24261112f, c3 = 0.05517167f;
+  unpack_f32x2(z, x, y);
+  z = pack_f32x2(fmaxf(x, -126.0f), fmaxf(y, -126.0f));
+  const uint64_t n = add_f32x2(z, pack_f32x2(kRound, kRound));
+  const uint64_t f =
+      fma_f32x2(add_f32x2(n, pack_f32x2(-kRound, -kRound)), pack_f32x2(-1.0f, -1.0f), z);
+  uint64_t r = fma_f32x2(f, pack_f32x2(c3, c3), pack_f32x2(c2, c2));
+  r = fma_f32x2(f, r, pack_f32x2(c1, c1));
+  r = fma_f32x2(f, r, pack_f32x2(c0, c0));
+  float u, v;
+  unpack_f32x2(r, x, y);
+  unpack_f32x2(n, u, v);
+  x = __int_as_float(__float_as_int(x) + (__float_as_int(u) << 23));
+  y = __int_as_float(__float_as_int(y) + (__float_as_int(v) << 23));
+}
+
 constexpr int kAttnTcThreads = 384;
 constexpr int kAttnTcTarget = 148;     // splits wanted: one per SM
 constexpr int kAttnTcKeys = 128;       // keys per block
+constexpr int kAttnTcPoly = 4;         // every fourth pair of powers on the fp32 pipe
 constexpr float kAttnTcLazy = 8.0f;    // growth of a row's maximum that rescales O
+
+constexpr int kAttnTcList = 8;         // items laid out at a time
+
+struct AttnTcItem {
+  int b, c0, head, slot, row0, nrows, past, kv_end;
+  int blk0, count, tail, fix;          // blocks blk0 .. blk0 + count - 1; count < 0: no item
+  int cnt[2];                          // blocks of each tile
+};
 
 template <int DP>
 struct AttnTcConfig {
@@ -123,9 +172,11 @@ struct AttnTcConfig {
   static constexpr int SLOTS = DP == 128 ? 5 : 8;
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
-  static constexpr int NUM_BARS = 2 * SLOTS + 10;
+  static constexpr int NUM_BARS = 2 * SLOTS + 16;
   static constexpr int OFF_PLAN = OFF_BAR + NUM_BARS * 8 + 16;
-  static constexpr int SMEM = OFF_PLAN + (int)sizeof(PlanShared) + 1024;   // + alignment slack
+  static constexpr int OFF_ITEMS = OFF_PLAN + (int)((sizeof(PlanShared) + 15) & ~15u);
+  static constexpr int SMEM =
+      OFF_ITEMS + kAttnTcList * (int)sizeof(AttnTcItem) + 1024;            // + alignment slack
   static constexpr uint32_t S_COL = 0, O_COL = 256;          // + 128 T
   static_assert(OFF_PLAN % 16 == 0 && SMEM <= 227 * 1024, "shared memory");
 };
@@ -141,27 +192,31 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full = bars;                         // slot filled (TMA bytes)
   uint64_t* empty = full + C::SLOTS;             // slot read (tcgen05.commit)
-  uint64_t* qfull = empty + C::SLOTS;            // both Q tiles written (8 warps)
-  uint64_t* sfull = qfull + 1;                   // [T] scores ready (commit)
-  uint64_t* pfull = sfull + 2;                   // [T] probabilities written (4 warps)
-  uint64_t* odone = pfull + 2;                   // [T] product with V done (commit)
+  uint64_t* qfull = empty + C::SLOTS;            // [T] Q tile written (4 warps)
+  uint64_t* turn = qfull + 2;                    // [T] tile T may use the tensor core (issuer)
+  uint64_t* sfull = turn + 2;                    // [T] scores ready (commit)
+  uint64_t* pfull = sfull + 2;                   // [T][half] probabilities written (4 warps)
+  uint64_t* odone = pfull + 4;                   // [T] product with V done (commit)
   uint64_t* vlast = odone + 2;                   // the block with the last key is here (issuer)
   uint64_t* vfix = vlast + 1;                    // its rows past that key are zeroed (warp 10)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   PlanShared& plan = *reinterpret_cast<PlanShared*>(smem + C::OFF_PLAN);
+  AttnTcItem* items = reinterpret_cast<AttnTcItem*>(smem + C::OFF_ITEMS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int D = p.D;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::SLOTS; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);
     }
-    mbar_init(qfull, 8);
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&qfull[t], 4);
+      mbar_init(&turn[t], 1);
       mbar_init(&sfull[t], 1);
-      mbar_init(&pfull[t], 4);
+      mbar_init(&pfull[2 * t], 4);
+      mbar_init(&pfull[2 * t + 1], 4);
       mbar_init(&odone[t], 1);
     }
     mbar_init(vlast, 1);
@@ -183,89 +238,119 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
   const uint32_t tbase = *tmem_slot;
   make_plan(p, plan);
 
-  uint32_t slot_it = 0;                          // ring position (producer, MMA, warp 10)
-  uint32_t items_done = 0, fixes = 0;
+  uint32_t slot_it = 0;                          // ring position (producer, issuers, warp 10)
+  uint32_t items_done = 0, fixes = 0, both_done = 0;
   uint32_t blocks_done[2] = {0, 0};              // blocks of tile T so far
 
-  // Every role walks the same items; `role` does its part of one.
-  struct Item {
-    SeqWork w;
-    int b, head, slot, row0, nrows, past, kv_end, blk0, count, tail;
-    int cnt[2];                                  // blocks of each tile
-    bool fix;
-  };
+  // Every role walks the same items, each at its own pace: the barriers above
+  // are all that ties them, so the producer fetches the next item's keys while
+  // the softmax still writes the last one's rows.  Only the list of items is
+  // common, laid out kAttnTcList at a time.
   auto walk = [&](auto&& role) {
-    for (int wave = 0;; ++wave) {
-      // items come longest first: every other wave runs the other way round,
-      // so that a CTA's share evens out
-      const int at = (wave & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
-      const long long c = (long long)wave * gridDim.x + at;
-      if ((long long)wave * gridDim.x >= plan.total) break;
-      if (c >= plan.total) continue;
-      find_item(p, plan, (int)c);
-      if (plan.b >= 0) {
-        Item job;
-        job.w = plan.w;
-        job.b = plan.b;
-        job.slot = plan.slot;
-        int tile, split;
-        item_place(p, job.w, plan.local, plan.splits, tile, job.head, split);
-        job.row0 = tile * C::RT;
-        job.nrows = min(C::RT, job.w.n * p.G - job.row0);
-        job.past = job.w.len - job.w.n;
-        job.kv_end = max(0, job.past + (job.row0 + job.nrows - 1) / p.G + 1);
-        const int blocks = (job.kv_end + kAttnTcKeys - 1) / kAttnTcKeys;
-        job.blk0 = (int)((long long)blocks * split / plan.splits);
-        const int blk1 = (int)((long long)blocks * (split + 1) / plan.splits);
-        // tile 0 ends with the keys its last row sees
-        const int last0 = job.row0 + min(job.nrows, 128) - 1;
-        const int end0 = (max(0, job.past + last0 / p.G + 1) + kAttnTcKeys - 1) / kAttnTcKeys;
-        job.cnt[0] = max(0, min(blk1, end0) - job.blk0);
-        job.cnt[1] = job.nrows > 128 ? blk1 - job.blk0 : 0;
-        job.count = max(job.cnt[0], job.cnt[1]);
-        // the block that holds the last key needs its value rows past it zeroed
-        job.tail = job.kv_end - (job.blk0 + job.count - 1) * kAttnTcKeys;
-        job.fix = job.count > 0 && job.tail < kAttnTcKeys;
+    for (int wave = 0; (long long)wave * gridDim.x < plan.total; wave += kAttnTcList) {
+      __syncthreads();                           // the last list is done with
+      if (threadIdx.x < kAttnTcList) items[threadIdx.x].count = -1;
+      __syncthreads();
+      for (int k = 0; k < kAttnTcList; ++k) {
+        // items come longest first: every other wave runs the other way round,
+        // so that a CTA's share evens out
+        const int at = ((wave + k) & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+        const long long c = (long long)(wave + k) * gridDim.x + at;
+        AttnTcItem& job = items[k];
+        if (c < plan.total)
+          find_item_as(p, plan, (int)c, [&](int b, const SeqWork& w, int local, int splits,
+                                            int slot) {
+            int tile, split;
+            item_place(p, w, local, splits, tile, job.head, split);
+            job.b = b;
+            job.c0 = w.c0;
+            job.slot = slot;
+            job.row0 = tile * C::RT;
+            job.nrows = min(C::RT, w.n * p.G - job.row0);
+            job.past = w.len - w.n;
+            job.kv_end = max(0, job.past + (job.row0 + job.nrows - 1) / p.G + 1);
+            const int blocks = (job.kv_end + kAttnTcKeys - 1) / kAttnTcKeys;
+            job.blk0 = (int)((long long)blocks * split / splits);
+            const int blk1 = (int)((long long)blocks * (split + 1) / splits);
+            // tile 0 ends with the keys its last row sees
+            const int last0 = job.row0 + min(job.nrows, 128) - 1;
+            const int end0 =
+                (max(0, job.past + last0 / p.G + 1) + kAttnTcKeys - 1) / kAttnTcKeys;
+            job.cnt[0] = max(0, min(blk1, end0) - job.blk0);
+            job.cnt[1] = job.nrows > 128 ? blk1 - job.blk0 : 0;
+            job.count = max(job.cnt[0], job.cnt[1]);
+            // the block that holds the last key needs its value rows past it zeroed
+            job.tail = job.kv_end - (job.blk0 + job.count - 1) * kAttnTcKeys;
+            job.fix = job.count > 0 && job.tail < kAttnTcKeys;
+          });
+      }
+      __syncthreads();
+      for (int k = 0; k < kAttnTcList; ++k) {
+        const AttnTcItem job = items[k];
+        if (job.count < 0) continue;
         role(job);
         slot_it += 2 * job.count;
         blocks_done[0] += job.cnt[0];
         blocks_done[1] += job.cnt[1];
+        both_done += min(job.cnt[0], job.cnt[1]);
         ++items_done;
         if (job.fix) ++fixes;
+        if (*abort_flag) break;
       }
-      tc_fence_before();
-      __syncthreads();                           // plan, Q tiles and tensor memory are free
-      tc_fence_after();
-      if (*abort_flag) break;
+      if (__syncthreads_or(*abort_flag)) break;
     }
   };
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    walk([&](const Item& job) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    walk([&](const AttnTcItem& job) {
       // --------------------------------------------------------- softmax
       const int t = warp >> 2, r = threadIdx.x & 127;        // tile and row in it
       const int row = 128 * t + r;                           // of the item
       const bool live = row < job.nrows;
-      const int gr = job.row0 + (live ? row : 0);
-      const long long off =
-          ((long long)(job.w.c0 + gr / p.G) * p.qh + (long long)job.head * p.G + gr % p.G) * D;
-      {
-        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.Q) + off;
-        uint8_t* dst = smem + t * C::TILE + r * 128;
+      // Rows move 16 bytes a lane, so that a warp takes whole rows at a time:
+      // LR lanes per row, rows sub, sub + 32 / LR, ... of the warp's 32.
+      constexpr int LR = DP / 8, STEP = 32 / LR;
+      const int ch = lane % LR, sub = lane / LR, wrow = 32 * (warp & 3);
+      uint8_t* qtile = smem + t * C::TILE + (ch >> 3) * C::SUB;
+      // element offset of the first such row, and the way to the next
+      const int gr0 = job.row0 + 128 * t + wrow + sub;
+      const int tok0 = gr0 / p.G, g0 = gr0 - tok0 * p.G;
+      const int tok_step = STEP / p.G, g_step = STEP - tok_step * p.G;
+      auto each_row = [&](auto&& f) {
+        int tok = tok0, g = g0;
 #pragma unroll
-        for (int ch = 0; ch < DP / 8; ++ch) {
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (live && 8 * ch < D) u = *reinterpret_cast<const uint4*>(src + 8 * ch);
-          *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::SUB + (((ch & 7) ^ (r & 7)) << 4)) = u;
+        for (int k = 0; k < LR; ++k) {
+          f(k, ((long long)(job.c0 + tok) * p.qh + (long long)job.head * p.G + g) * D + 8 * ch);
+          tok += tok_step;
+          g += g_step;
+          if (g >= p.G) {
+            g -= p.G;
+            ++tok;
+          }
+        }
+      };
+      {
+        uint4 u[LR];
+        each_row([&](int k, long long off) {
+          u[k] = make_uint4(0, 0, 0, 0);
+          if (128 * t + wrow + sub + STEP * k < job.nrows && 8 * ch < D)
+            u[k] = *reinterpret_cast<const uint4*>(
+                reinterpret_cast<const __nv_bfloat16*>(p.Q) + off);
+        });
+#pragma unroll
+        for (int k = 0; k < LR; ++k) {
+          const int rr = wrow + sub + STEP * k;
+          *reinterpret_cast<uint4*>(qtile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = u[k];
         }
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(qfull);
+        if (lane == 0) mbar_arrive(&qfull[t]);
       }
       const uint32_t lanes = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
       const uint32_t scol = lanes + C::S_COL + 128u * t, ocol = lanes + C::O_COL + 128u * t;
-      const int lim = live ? job.past + gr / p.G + 1 : 0;        // keys this row sees
+      // keys this row sees
+      const int lim = live ? job.past + (job.row0 + row) / p.G + 1 : 0;
       // keys that the warp's rows all see
       const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
       float m = -INFINITY;                                   // reference, log2 units
@@ -283,7 +368,8 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(scol + 32u * q, s[q]);
         tmem_ld_wait();
         const int key0 = (job.blk0 + i) * kAttnTcKeys;
-        if (key0 + kAttnTcKeys > lim_warp) {
+        const bool masked = key0 + kAttnTcKeys > lim_warp;
+        if (masked) {
           const int n = lim - key0;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -294,58 +380,81 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         float mx[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          mx[q] = __uint_as_float(s[q][0]);
+          mx[q] = max3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]),
+                       __uint_as_float(s[q][2]));
 #pragma unroll
-          for (int k = 1; k < 32; ++k) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][k]));
+          for (int k = 3; k < 31; k += 2)
+            mx[q] = max3(mx[q], __uint_as_float(s[q][k]), __uint_as_float(s[q][k + 1]));
+          mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
         }
         const float mnew =
             fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        if (i == 0) {
-          m = mnew;
-        } else {
+        if (i == 0) m = mnew;
+        // The first half's powers are taken relative to the reference of the
+        // blocks before, beside the search for this block's maximum; only if
+        // that turns out to have outgrown the reference are they taken again.
+        const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+        uint64_t lh = 0;
+        uint32_t ph[32];
+        auto powers = [&](int half, float base, auto all_seen) {
+          const uint64_t base2 = pack_f32x2(base, base);
+          lh = 0;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int q = 2 * half + (k >> 4), e = 2 * (k & 15);
+            const uint64_t z = fma_f32x2(
+                pack_f32x2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), scale2, base2);
+            float u, v;
+            if (decltype(all_seen)::value && k % kAttnTcPoly == kAttnTcPoly - 1) {
+              ex2_poly2(z, u, v);
+            } else {
+              unpack_f32x2(z, u, v);
+              u = ex2(u);
+              v = ex2(v);
+            }
+            lh = add_f32x2(lh, pack_f32x2(u, v));
+            ph[k] = pack_bf16x2(u, v);
+          }
+        };
+        auto hand_over = [&](int half) {
+          tmem_st_32x32b_x32(scol + 32u * half, ph);
+          l2 = add_f32x2(l2, lh);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[2 * t + half]);
+        };
+        auto block = [&](auto all_seen) {
+          float base = m == -INFINITY ? 0.0f : -m;
+          powers(0, base, all_seen);
           const bool grow = mnew > m + kAttnTcLazy || (m == -INFINITY && mnew != -INFINITY);
           if (__any_sync(0xffffffffu, grow)) {
-            const float next = grow ? mnew : m;
             const float f = grow ? ex2(m - mnew) : 1.0f;
             l2 = fma_f32x2(l2, pack_f32x2(f, f), 0);
-            m = next;
+            if (grow) m = mnew;
+            base = m == -INFINITY ? 0.0f : -m;
             // the product of the last block is done: its completion precedes
             // that of the scores just read
 #pragma unroll 1
-            for (int d = 0; d < DP; d += 32) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(ocol + d, o);
+            for (int d = 0; d < DP; d += 16) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(ocol + d, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st_32x32b_x32(ocol + d, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st_32x32b_x16(ocol + d, o);
             }
             tmem_st_wait();
+            powers(0, base, all_seen);
           }
-        }
-        const float base = m == -INFINITY ? 0.0f : -m;
-        const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
-        const uint64_t base2 = pack_f32x2(base, base);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t ph[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x, y;
-            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[q][2 * k]),
-                                              __uint_as_float(s[q][2 * k + 1])), scale2, base2),
-                         x, y);
-            x = ex2(x);
-            y = ex2(y);
-            l2 = add_f32x2(l2, pack_f32x2(x, y));
-            ph[k] = pack_bf16x2(x, y);
-          }
-          tmem_st_32x32b_x16(scol + 16u * q, ph);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[t]);
+          hand_over(0);
+          powers(1, base, all_seen);
+          hand_over(1);
+        };
+        if (masked)
+          block(std::false_type{});
+        else
+          block(std::true_type{});
       }
       // ---- the rows' sums
       float l, lb;
@@ -376,22 +485,32 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[k + e]) * inv;
-            if (live && d + k < D) {
-              if (job.slot >= 0)
-                store_f32<8>(part + 2 * C::RT + (long long)row * D + d + k, x);
-              else
-                store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(p.O) + off + d + k, x);
+            if (job.slot >= 0) {
+              if (live && d + k < D) store_f32<8>(part + 2 * C::RT + (long long)row * D + d + k, x);
+            } else {                             // through the Q tile, which is done with
+              store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(
+                                smem + t * C::TILE + ((d + k) >> 6) * C::SUB + r * 128 +
+                                ((((d + k) >> 3 & 7) ^ (r & 7)) << 4)), x);
             }
           }
+        }
+        if (job.slot < 0) {
+          __syncwarp();
+          each_row([&](int k, long long off) {
+            const int rr = wrow + sub + STEP * k;
+            if (128 * t + rr < job.nrows && 8 * ch < D)
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.O) + off) =
+                  *reinterpret_cast<const uint4*>(qtile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+          });
           __syncwarp();
         }
       }
       tc_fence_before();
     });
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
-      walk([&](const Item& job) {
+      walk([&](const AttnTcItem& job) {
       // -------------------------------------------------------- producer
       const int pieces = kAttnTcKeys / box_rows;             // loads per block and 64 columns
       bool ok = true;
@@ -426,73 +545,119 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         }
       }
       });
-    } else if (warp == 9) {
-      walk([&](const Item& job) {
-      // ------------------------------------------------------ MMA issuer
-      if (lane == 0 && job.count > 0) {
+    } else if (warp == 9 || warp == 11) {
+      const int t = warp == 9 ? 0 : 1;
+      walk([&](const AttnTcItem& job) {
+      // -------------------------------------------------- MMA issuer, tile t
+      // One issuer per tile: each waits for its own probabilities while the
+      // tensor core works for the other (one issuer for both in turn left it
+      // idle half of the time).  The whole warp follows the loop and one
+      // elected lane issues, so that descriptors live in uniform registers.
+      // Each barrier is waited for in every one of its phases, needed or not: a
+      // parity wait that skips one may take the phase before for its own.
+      bool ok = __all_sync(0xffffffffu, mbar_wait(&qfull[t], items_done & 1u, abort_flag));
+      if (job.count > 0) {
         constexpr uint32_t idesc_s = make_idesc_bf16(128, 128, false);
         constexpr uint32_t idesc_o = make_idesc_bf16(128, DP, true);
-        const uint32_t qa = smem_u32(smem), kva = qa + C::OFF_KV;
-        auto scores = [&](int t, uint32_t ka) {
+        const bool leader = elect_one();
+        const uint32_t kva = smem_u32(smem) + C::OFF_KV;
+        const uint64_t qd = make_sdesc_sw128(smem_u32(smem) + t * C::TILE);
+        const uint32_t dcol = tbase + C::O_COL + 128u * t, scol = tbase + C::S_COL + 128u * t;
+        const int cnt = t == 0 ? job.cnt[0] : job.cnt[1];
+        const uint32_t done0 = t == 0 ? blocks_done[0] : blocks_done[1];
+        const int both = min(job.cnt[0], job.cnt[1]);
+        const bool last_here = cnt == job.count && (t == 1 || job.cnt[1] < job.count);
+        auto scores = [&](uint32_t st) {
+          const uint64_t kd = make_sdesc_sw128(kva + st * C::TILE);
+          if (leader) {
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const uint32_t o = (uint32_t)((k >> 2) * C::SUB + 32 * (k & 3));
-            mma_f16_ss(tbase + C::S_COL + 128u * t, make_sdesc_sw128(qa + t * C::TILE + o),
-                       make_sdesc_sw128(ka + o), idesc_s, k != 0);
+            for (int k = 0; k < DP / 16; ++k) {
+              const uint64_t o = (uint64_t)((k >> 2) * (C::SUB >> 4) + 2 * (k & 3));
+              mma_f16_ss(scol, qd + o, kd + o, idesc_s, k != 0);
+            }
+            tc_commit(&sfull[t]);
+            tc_commit(&empty[st]);
           }
-          tc_commit(&sfull[t]);
+          __syncwarp();
         };
-        bool ok = mbar_wait(qfull, items_done & 1u, abort_flag);
         uint32_t it = slot_it;
+        // a slot is free once both issuers have let go of it
         ok = ok && mbar_wait(&full[it % C::SLOTS], (it / C::SLOTS) & 1u, abort_flag);
-        if (ok) {
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && cnt > 0) {
           tc_fence_after();
-          for (int t = 0; t < 2; ++t)
-            if (job.cnt[t] > 0) scores(t, kva + (it % C::SLOTS) * C::TILE);
-          tc_commit(&empty[it % C::SLOTS]);
-          ++it;
+          scores(it % C::SLOTS);
+        } else if (ok && lane == 0) {
+          mbar_arrive(&empty[it % C::SLOTS]);
         }
-        for (int i = 0; ok && i < job.count; ++i) {
+        ++it;
+        for (int i = 0; ok && i < job.count; ++i, it += 2) {
           const uint32_t sv = it % C::SLOTS, sk = (it + 1) % C::SLOTS;
-          if (!mbar_wait(&full[sv], (it / C::SLOTS) & 1u, abort_flag)) break;
-          if (job.fix && i == job.count - 1) {
-            mbar_arrive(vlast);
-            if (!mbar_wait(vfix, fixes & 1u, abort_flag)) break;
-          }
           const bool more = i + 1 < job.count;
-          bool kready = false;
-          for (int t = 0; t < 2; ++t) {
-            if (i >= job.cnt[t]) continue;
-            const uint32_t nth = blocks_done[t] + i;
-            if (!(ok = mbar_wait(&pfull[t], nth & 1u, abort_flag))) break;
-            tc_fence_after();
+          if (i >= cnt) {                        // the other tile sees more keys
+            ok = mbar_wait(&full[sv], (it / C::SLOTS) & 1u, abort_flag);
+            if (job.fix && !more) ok = ok && mbar_wait(vfix, fixes & 1u, abort_flag);
+            if (ok && lane == 0) mbar_arrive(&empty[sv]);
+            if (more) {
+              ok = ok && mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag);
+              if (ok && lane == 0) mbar_arrive(&empty[sk]);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            continue;
+          }
+          ok = mbar_wait(&full[sv], (it / C::SLOTS) & 1u, abort_flag);
+          if (job.fix && !more) {
+            if (ok && leader && last_here) mbar_arrive(vlast);
+            ok = ok && mbar_wait(vfix, fixes & 1u, abort_flag);
+          }
+          const uint64_t vd = make_sdesc_mn_sw128(kva + sv * C::TILE, C::SUB);
+          // While both tiles have blocks they take turns of one product with V
+          // and the next scores: one tile's runs while the other is in the
+          // softmax.  The first half of the keys goes ahead of the second.
+          const uint32_t nth = both_done + i;
+          const bool turns = i < both;
 #pragma unroll
-            for (int k = 0; k < kAttnTcKeys / 16; ++k)
-              mma_f16_ts(tbase + C::O_COL + 128u * t, tbase + C::S_COL + 128u * t + 8u * k,
-                         make_sdesc_mn_sw128(kva + sv * C::TILE + 2048u * k, C::SUB), idesc_o,
-                         (i | k) != 0);
-            tc_commit(&odone[t]);
-            if (i + 1 < job.cnt[t]) {
-              if (!kready) {
-                if (!(ok = mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag))) break;
-                kready = true;
-              }
-              // the scores overwrite the probabilities the product reads
-              if (!(ok = mbar_wait(&odone[t], nth & 1u, abort_flag))) break;
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && mbar_wait(&pfull[2 * t + h], (done0 + i) & 1u, abort_flag);
+            if (h == 0 && turns && (t == 1 || nth > 0))
+              ok = ok && mbar_wait(&turn[t], (t == 0 ? nth - 1 : nth) & 1u, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
               tc_fence_after();
-              scores(t, kva + sk * C::TILE);
+              if (leader) {
+#pragma unroll
+                for (int k = 4 * h; k < 4 * h + 4; ++k)
+                  mma_f16_ts(dcol, scol + 8u * k, vd + (uint64_t)(128 * k), idesc_o,
+                             k == 0 ? i != 0 : 1);
+                if (h == 1) {
+                  tc_commit(&odone[t]);
+                  tc_commit(&empty[sv]);
+                }
+              }
+              __syncwarp();
             }
           }
-          if (!ok) break;
-          tc_commit(&empty[sv]);
-          if (more) tc_commit(&empty[sk]);
-          it += 2;
+          if (more && i + 1 < cnt) {
+            ok = ok && mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag);
+            // the scores overwrite the probabilities the product reads
+            ok = ok && mbar_wait(&odone[t], (done0 + i) & 1u, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              tc_fence_after();
+              scores(sk);
+            }
+          } else if (more) {
+            ok = ok && mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && lane == 0) mbar_arrive(&empty[sk]);
+          }
+          if (ok && turns && leader) mbar_arrive(&turn[1 - t]);
         }
       }
       __syncwarp();
       });
     } else if (warp == 10) {
-      walk([&](const Item& job) {
+      walk([&](const AttnTcItem& job) {
       // ------------------------------------------ value rows past the end
       if (job.fix) {
         const uint32_t it = slot_it + 2 * job.count - 1;
@@ -509,17 +674,16 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         if (lane == 0) mbar_arrive(vfix);
       }
       });
-    } else {
-      walk([&](const Item&) {});
     }
   }
 
   // Never leave tensor-core work or bulk copies in flight (an abort can).
   if (*abort_flag) {
-    if (warp == 9 && lane == 0) {
-      tc_commit(&odone[0]);
-      mbar_wait(&odone[0], 0, nullptr, 100000000ull);
-      mbar_wait(&odone[0], 1, nullptr, 100000000ull);
+    if ((warp == 9 || warp == 11) && elect_one()) {
+      uint64_t* bar = &odone[warp == 9 ? 0 : 1];
+      tc_commit(bar);
+      mbar_wait(bar, 0, nullptr, 100000000ull);
+      mbar_wait(bar, 1, nullptr, 100000000ull);
     }
     if (warp == 8 && lane == 0) {
       const uint32_t last = slot_it < (uint32_t)C::SLOTS ? slot_it : (uint32_t)C::SLOTS;
