@@ -253,75 +253,82 @@ def alloc_block_tail_workspace(M, H, I, device="cuda"):
                        device=device)
 
 
+# The serving calls check shapes, types and devices here (the C side sees only
+# pointers).  They run once per layer and token, so the checks are written to
+# cost little: one pass over the tensors, messages formed only on failure.
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
-def _one_device(stream, **tensors):
-    """Every tensor on one CUDA device, the current one: the launch goes there."""
-    current = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for name, t in tensors.items():
+def _device_ptrs(names, tensors):
+    """Addresses of contiguous tensors (None for None), all on the current CUDA device, where
+    the launch goes."""
+    try:
+        index = torch.cuda.current_device()
+    except (AssertionError, RuntimeError):
+        index = -2
+    out = []
+    for t in tensors:
         if t is None:
-            continue
-        _need(t.is_cuda, f"{name} must live on a CUDA device")
-        _need(t.device.index == current,
-              f"{name} is on {t.device}, the current device is cuda:{current}")
+            out.append(None)
+        elif t.get_device() == index and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            name = names.split()[len(out)]
+            _need(t.is_cuda, f"{name} must live on a CUDA device")
+            _need(t.get_device() == index, f"{name} is on {t.device}, not on the current device")
+            _need(False, f"{name} must be contiguous")
+    return out
 
 
-def _int32(name, t, *shape):
-    _need(t.dtype == torch.int32 and tuple(t.shape) == shape,
-          f"{name} must be int32 of shape {list(shape)}")
-
-
-def _rows(name, t, width, dtype):
-    """Pointer and row stride of a matrix whose rows are contiguous."""
-    _need(t.dim() == 2 and t.shape[1] == width and t.dtype == dtype,
+def _rows(name, t, width, dtype, device):
+    """Address and row stride of a matrix whose rows are contiguous."""
+    _need(t.dim() == 2 and t.dtype == dtype and t.shape[1] == width,
           f"{name} must be [M][{width}] of {dtype}")
-    _need(t.shape[1] == 1 or t.stride(1) == 1, f"the rows of {name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), (width if t.shape[0] <= 1 else t.stride(0))
+    _need(t.get_device() == device, f"{name} must live on Q_out's device")
+    row, col = t.stride()
+    _need(col == 1 or width == 1, f"the rows of {name} must be contiguous")
+    return t.data_ptr(), (row if t.shape[0] > 1 else width)
 
 
 def _paged(cu_q, kv_len, block_table, k_cache, v_cache):
     """(batch, table_stride, num_pages, kv_heads, page_size, head_dim) of a paged cache."""
-    _need(k_cache.dim() == 4 and k_cache.dtype == torch.bfloat16 and
-          v_cache.dtype == torch.bfloat16 and k_cache.shape == v_cache.shape,
+    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and
+          k_cache.dtype == torch.bfloat16 and v_cache.dtype == torch.bfloat16,
           "k_cache and v_cache must be bf16 [num_pages][kv_heads][page_size][head_dim]")
     batch = kv_len.numel()
-    _int32("kv_len", kv_len, batch)
-    _int32("cu_q", cu_q, batch + 1)
-    _need(block_table.dim() == 2, "block_table must be [batch][table_stride]")
-    _int32("block_table", block_table, batch, block_table.shape[1])
+    _need(kv_len.dtype == cu_q.dtype == block_table.dtype == torch.int32,
+          "cu_q, kv_len and block_table must be int32")
+    _need(kv_len.dim() == 1 and cu_q.dim() == 1 and cu_q.numel() == batch + 1 and
+          block_table.dim() == 2 and block_table.shape[0] == batch,
+          "kv_len must be [batch], cu_q [batch + 1], block_table [batch][table_stride]")
     pages, heads, page, dim = k_cache.shape
     return batch, block_table.shape[1], pages, heads, page, dim
-
-
-def _gain(name, t, dim):
-    if t is not None:
-        _need(t.dtype == torch.float32 and t.numel() == dim, f"{name} must be fp32 [{dim}]")
-    return _ptr(t)
 
 
 def bitnet_linear_w8(Xq, x_scale, Wq, w_scale, Y, silu=False, residual=None, epilogue=None,
                      stream=None):
     """Y [M][N] = (Xq . Wq^T) / (x_scale[m] w_scale[n]) (int32 Y: the sum itself), the codes
     and scales of both sides from bitnet_quant_act (see include/bitnet.h)."""
-    _one_device(stream, Xq=Xq, x_scale=x_scale, Wq=Wq, w_scale=w_scale, Y=Y, residual=residual)
+    xq, xs, wq, ws, y, res = _device_ptrs("Xq x_scale Wq w_scale Y residual",
+                                          (Xq, x_scale, Wq, w_scale, Y, residual))
     _need(Xq.dim() == 2 and Wq.dim() == 2 and Xq.dtype == Wq.dtype == torch.int8 and
           Xq.shape[1] == Wq.shape[1], "Xq and Wq must be int8 [M][K] and [N][K]")
     (M, K), N = Xq.shape, Wq.shape[0]
     _need(x_scale.dtype == w_scale.dtype == torch.float32 and x_scale.numel() == M and
           w_scale.numel() == N, "x_scale and w_scale must be fp32 [M] and [N]")
-    _need(tuple(Y.shape) == (M, N), f"Y must be [{M}][{N}]")
-    if residual is not None:
-        _need(residual.shape == Y.shape and residual.dtype == Y.dtype,
-              "residual must have Y's shape and type")
+    _need(Y.shape == (M, N), "Y must be [M][N]")
+    _need(residual is None or (residual.shape == Y.shape and residual.dtype == Y.dtype),
+          "residual must have Y's shape and type")
+    kind = _dtype(Y)
     if epilogue is None:
-        epilogue = (_dtype(Y) | (BITNET_EPI_SILU if silu else 0) |
+        epilogue = (kind | (BITNET_EPI_SILU if silu else 0) |
                     (BITNET_EPI_RESIDUAL if residual is not None else 0))
-    _need((epilogue & BITNET_EPI_TYPE_MASK) == _dtype(Y), "epilogue names another type than Y's")
-    _check(library().bitnet_linear_w8(_ptr(Xq), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), M, N, K,
-                                      _ptr(Y), int(epilogue), _ptr(residual), _stream(stream)))
+    _need((epilogue & BITNET_EPI_TYPE_MASK) == kind, "epilogue names another type than Y's")
+    _check(library().bitnet_linear_w8(xq, xs, wq, ws, M, N, K, y, epilogue, res,
+                                      _stream(stream)))
 
 
 def bitnet_rope_append(Q, K, V, inv_freq, cu_q, kv_len, block_table, k_cache, v_cache, Q_out,
@@ -330,24 +337,26 @@ def bitnet_rope_append(Q, K, V, inv_freq, cu_q, kv_len, block_table, k_cache, v_
     """Rotate the new tokens' queries (into Q_out) and keys and append keys and values to the
     paged cache (see include/bitnet.h).  Q, K, V are [M][heads * head_dim]; their rows may be
     strided (slices of one fused projection)."""
-    _one_device(stream, Q=Q, K=K, V=V, inv_freq=inv_freq, cu_q=cu_q, kv_len=kv_len,
-                block_table=block_table, k_cache=k_cache, v_cache=v_cache, Q_out=Q_out,
-                q_gain=q_gain, k_gain=k_gain)
+    inv, cu, length, table, kc, vc, out, qg, kg = _device_ptrs(
+        "inv_freq cu_q kv_len block_table k_cache v_cache Q_out q_gain k_gain",
+        (inv_freq, cu_q, kv_len, block_table, k_cache, v_cache, Q_out, q_gain, k_gain))
     batch, stride, pages, heads, page, dim = _paged(cu_q, kv_len, block_table, k_cache, v_cache)
-    M, width = Q.shape
-    q, ldq = _rows("Q", Q, width, Q.dtype)
-    k, ldk = _rows("K", K, heads * dim, Q.dtype)
-    v, ldv = _rows("V", V, heads * dim, Q.dtype)
-    _need(width % dim == 0 and K.shape[0] == V.shape[0] == M,
-          "Q, K and V must have the same rows, of whole heads")
-    _need(Q_out.shape == Q.shape and Q_out.dtype == Q.dtype, "Q_out must have Q's shape and type")
+    dtype, device = Q_out.dtype, Q_out.get_device()
+    _need(Q_out.dim() == 2 and Q_out.shape[1] % dim == 0,
+          "Q_out must be [M][q_heads * head_dim]")
+    M, width = Q_out.shape
+    q, ldq = _rows("Q", Q, width, dtype, device)
+    k, ldk = _rows("K", K, heads * dim, dtype, device)
+    v, ldv = _rows("V", V, heads * dim, dtype, device)
+    _need(Q.shape[0] == K.shape[0] == V.shape[0] == M, "Q, K, V and Q_out must have the same rows")
     _need(inv_freq.dtype == torch.float32, "inv_freq must be fp32")
-    flags = int(rope) | (BITNET_ROPE_HEAD_NORM if head_norm else 0)
+    for g in (q_gain, k_gain):
+        _need(g is None or (g.dtype == torch.float32 and g.numel() == dim),
+              "gains must be fp32 [head_dim]")
     _check(library().bitnet_rope_append(
-        q, ldq, k, ldk, v, ldv, _dtype(Q), M, width // dim, heads, dim, _ptr(inv_freq),
-        2 * inv_freq.numel(), flags, _gain("q_gain", q_gain, dim), _gain("k_gain", k_gain, dim),
-        float(eps), batch, _ptr(cu_q), _ptr(kv_len), _ptr(block_table), stride, _ptr(k_cache),
-        _ptr(v_cache), pages, page, _ptr(Q_out), _stream(stream)))
+        q, ldq, k, ldk, v, ldv, _dtype(Q_out), M, width // dim, heads, dim, inv,
+        2 * inv_freq.numel(), rope | (BITNET_ROPE_HEAD_NORM if head_norm else 0), qg, kg, eps,
+        batch, cu, length, table, stride, kc, vc, pages, page, out, _stream(stream)))
 
 
 def bitnet_attention_workspace_size(M, batch, q_heads, kv_heads, head_dim):
@@ -366,17 +375,16 @@ def bitnet_attention(Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspac
                      stream=None):
     """Causal attention of the new tokens over the paged cache (see include/bitnet.h); scale is
     1 / sqrt(head_dim) unless given."""
-    _one_device(stream, Q=Q, cu_q=cu_q, kv_len=kv_len, block_table=block_table, k_cache=k_cache,
-                v_cache=v_cache, O=O, workspace=workspace)
+    q, cu, length, table, kc, vc, out, ws = _device_ptrs(
+        "Q cu_q kv_len block_table k_cache v_cache O workspace",
+        (Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspace))
     batch, stride, pages, heads, page, dim = _paged(cu_q, kv_len, block_table, k_cache, v_cache)
     _need(Q.dim() == 2 and Q.shape[1] % dim == 0, "Q must be [M][q_heads * head_dim]")
     _need(O.shape == Q.shape and O.dtype == Q.dtype, "O must have Q's shape and type")
-    if scale is None:
-        scale = dim ** -0.5
+    M, width = Q.shape
     _check(library().bitnet_attention(
-        _ptr(Q), _dtype(Q), Q.shape[0], Q.shape[1] // dim, heads, dim, float(scale), batch,
-        _ptr(cu_q), _ptr(kv_len), _ptr(block_table), stride, _ptr(k_cache), _ptr(v_cache), pages,
-        page, _ptr(O), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        q, _dtype(Q), M, width // dim, heads, dim, dim ** -0.5 if scale is None else scale, batch,
+        cu, length, table, stride, kc, vc, pages, page, out, ws, workspace.nbytes,
         _stream(stream)))
 
 

@@ -663,12 +663,10 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         const uint32_t it = slot_it + 2 * job.count - 1;
         mbar_wait(vlast, fixes & 1u, abort_flag);
         uint8_t* v = smem + C::OFF_KV + (it % C::SLOTS) * C::TILE;
-        for (int i = lane; i < (kAttnTcKeys - job.tail) * 8 * C::HALVES; i += 32) {
-          const int r = job.tail + (i >> 3) % (kAttnTcKeys - job.tail);
-          const int h = (i >> 3) / (kAttnTcKeys - job.tail);
-          *reinterpret_cast<uint4*>(v + h * C::SUB + r * 128 + (i & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
+        constexpr int LR = 8 * C::HALVES;          // lanes per row
+        v += ((lane >> 3) % C::HALVES) * C::SUB + (lane & 7) * 16;
+        for (int r = job.tail + lane / LR; r < kAttnTcKeys; r += 32 / LR)
+          *reinterpret_cast<uint4*>(v + r * 128) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(vfix);
