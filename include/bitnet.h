@@ -285,7 +285,8 @@ BITNET_API int bitnet_linear_w8(const int8_t *Xq, const float *x_scale, const in
  *             at a negative position has no place and is left out.
  * q_heads is a multiple of kv_heads; query head h reads key/value head
  * h / (q_heads / kv_heads).  head_dim is a multiple of 16 in [16, 256],
- * page_size a multiple of 16, table_stride * page_size at most 2^30.  The
+ * page_size a multiple of 16, table_stride * page_size and M * q_heads at most
+ * 2^30.  The
  * tables are device memory read on the stream, so a captured call follows
  * lengths that change between replays.  A page index, row or length out of
  * range is recorded in the device error word (bitnet_check_device_error()

@@ -16,12 +16,14 @@
 // t * G + g of a sequence is token t, head g of the group, so a tile reads
 // its keys and values once for all of them.
 //
-// Work: a tile of rows (RT) times one key/value head is an item; where the
-// batch has too few items to fill the GPU its keys are cut into splits of at
-// least `min_units` blocks, sized on the device from the lengths it finds
-// there (so a captured graph keeps fitting as the cache grows).  A split
-// writes its unnormalised sums and statistics to the workspace and the join
-// kernel adds them; an uncut item writes its rows directly.
+// Work: a tile of rows (RT) times one key/value head is an item, its blocks of
+// keys (and one more for its start and end) its length in units.  Where the
+// items are too few to deal out evenly, all units of the call are laid end to
+// end and cut into one equal share per CTA, on the device, from the lengths it
+// finds there (so a captured graph keeps fitting as the cache grows).  A CTA
+// whose share starts or ends inside an item writes unnormalised sums and
+// statistics to the workspace and the join kernel adds them; an item inside
+// one share is written directly.
 #pragma once
 
 #include "common.cuh"
@@ -31,8 +33,7 @@ namespace bitnet {
 
 constexpr int kAttnThreads = 128;
 constexpr int kAttnTile = 64;          // keys per block of the mma.sync kernel
-constexpr int kAttnTarget = 592;       // splits wanted over a call: four per SM
-constexpr int kAttnPlanHead = 4;       // words before the per-sequence slots of the plan
+constexpr int kAttnTarget = 592;       // most shares of a call (mma.sync kernel)
 
 struct AttnParams {
   PagedBatch pb;
@@ -41,18 +42,17 @@ struct AttnParams {
   const __nv_bfloat16 *Kc, *Vc;
   int qh, kvh, G, D;
   float scale_log2;                    // softmax scale * log2(e)
-  int RT;                              // rows per tile
-  int unit;                            // keys per block
-  int min_units;                       // smallest split, in blocks
-  int target;                          // splits wanted over the whole call, 0: never split
-  int* plan;                           // [0] blocks per split, [kAttnPlanHead + b] first slot of b
+  int rt_shift, unit_shift;            // log2 of the rows per tile and the keys per block
+  int min_units;                       // smallest share
+  int target;                          // shares wanted, 0: whole items, dealt out in turn
+  long long* plan;                     // [0] units per share, [1 + b] units before sequence b
   float* part;                         // slots: m[RT], l[RT], o[RT][D]
 };
 
 // --------------------------------------------------------------- the plan
 struct SeqWork {
   int c0, n, len;                      // first row, new tokens, cached tokens
-  int tiles, units;
+  int tiles, units;                    // row tiles; units of one item
 };
 
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool report) {
@@ -60,7 +60,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool rep
   w.c0 = __ldg(p.pb.cu_q + b);
   const int c1 = __ldg(p.pb.cu_q + b + 1);
   w.len = __ldg(p.pb.kv_len + b);
-  const long long cap = (long long)p.pb.stride * p.pb.page_size;
+  const int cap = p.pb.stride * p.pb.page_size;      // at most 2^30
   if (w.c0 < 0 || c1 < w.c0 || c1 > p.pb.M) {
     if (report) record_device_error(DEV_ERR_INDEX);
     w.c0 = 0;
@@ -70,146 +70,155 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool rep
   }
   if (w.len < 0 || w.len > cap) {
     if (report) record_device_error(DEV_ERR_INDEX);
-    w.len = w.len < 0 ? 0 : (int)cap;
+    w.len = w.len < 0 ? 0 : cap;
   }
-  w.tiles = (int)(((long long)w.n * p.G + p.RT - 1) / p.RT);
-  w.units = (w.len + p.unit - 1) / p.unit;
+  w.tiles = (w.n * p.G + (1 << p.rt_shift) - 1) >> p.rt_shift;
+  w.units = p.target > 0 ? ((w.len + (1 << p.unit_shift) - 1) >> p.unit_shift) + 1 : 1;
   return w;
-}
-
-__device__ __forceinline__ int splits_of(int units, int chunk) {
-  return units <= chunk ? 1 : (units + chunk - 1) / chunk;
 }
 
 // Thread t of the CTA holds sequences [t per, (t + 1) per) of the batch.
 struct PlanShared {
-  int chunk, total;
-  int items[kAttnThreads + 1];         // items before each thread's sequences
-  int slots[kAttnThreads + 1];
+  long long share, total;              // units per share, of the call
+  long long cursor;                    // where this CTA's share goes on
+  long long first[kAttnThreads + 1];   // units before each thread's sequences
   long long red[kAttnThreads / 32];
-  // the item that was looked up
-  int b, local, splits, slot;
-  SeqWork w;
 };
-
-// Inclusive scan over the first kAttnThreads threads' values (two at a time);
-// further threads of the CTA only keep the barriers.
-__device__ __forceinline__ void plan_scan(int& a, int& b, PlanShared& s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int o = 1; o < 32; o *= 2) {
-    const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-    if (lane >= o) {
-      a += x;
-      b += y;
-    }
-  }
-  if (lane == 31 && warp < kAttnThreads / 32) s.red[warp] = ((long long)b << 32) | (unsigned)a;
-  __syncthreads();
-  for (int i = 0; i < warp && i < kAttnThreads / 32; ++i) {
-    a += (int)(s.red[i] & 0xffffffffll);
-    b += (int)(s.red[i] >> 32);
-  }
-}
 
 // All threads of the CTA, kAttnThreads at least (sequences of later threads
 // would start past the batch: they hold none).
 __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
-  const int tid = threadIdx.x, B = p.pb.batch;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.pb.batch;
   const int per = (B + kAttnThreads - 1) / kAttnThreads;
   const int b0 = tid * per, b1 = min(B, b0 + per);
   const bool first = blockIdx.x == 0;
-  int chunk = 0x7fffffff;
-  if (p.target > 0) {
-    long long u = 0;
-    for (int b = b0; b < b1; ++b) {
-      const SeqWork w = seq_work(p, b, false);
-      u += (long long)w.tiles * w.units;
-    }
-    for (int o = 16; o > 0; o /= 2) u += __shfl_xor_sync(0xffffffffu, u, o);
-    if ((tid & 31) == 0 && tid < kAttnThreads) s.red[tid >> 5] = u;
-    __syncthreads();
-    u = 0;
-    for (int i = 0; i < kAttnThreads / 32; ++i) u += s.red[i];
-    const long long want = (u * p.kvh + p.target - 1) / p.target;
-    chunk = want < p.min_units ? p.min_units : want > 0x7ffffffell ? 0x7fffffff : (int)want;
-    __syncthreads();
-  }
-  int items = 0, slots = 0;
+  long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const SeqWork w = seq_work(p, b, first);
-    const int sp = splits_of(w.units, chunk);
-    items += w.tiles * p.kvh * sp;
-    if (sp > 1) slots += w.tiles * p.kvh * sp;
+    mine += (long long)w.tiles * p.kvh * w.units;
   }
-  const int mine = items, mine_s = slots;
-  plan_scan(items, slots, s);
-  if (tid < kAttnThreads) {
-    s.items[tid] = items - mine;
-    s.slots[tid] = slots - mine_s;
+  long long sum = mine;                // inclusive scan
+  for (int o = 1; o < 32; o *= 2) {
+    const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += x;
   }
-  if (tid == kAttnThreads - 1) {
-    s.items[kAttnThreads] = items;
-    s.total = items;
-    s.chunk = chunk;
+  if (lane == 31 && warp < kAttnThreads / 32) s.red[warp] = sum;
+  __syncthreads();
+  for (int i = 0; i < warp && i < kAttnThreads / 32; ++i) sum += s.red[i];
+  if (tid < kAttnThreads) s.first[tid] = sum - mine;
+  long long total = 0;
+  for (int i = 0; i < kAttnThreads / 32; ++i) total += s.red[i];
+  long long share = 1;
+  if (p.target > 0) {
+    long long shares = total / p.min_units;
+    shares = shares < 1 ? 1 : shares > p.target ? p.target : shares;
+    share = (total + shares - 1) / shares;
+    if (share < 1) share = 1;
+  }
+  if (tid == 0) {
+    s.first[kAttnThreads] = total;
+    s.total = total;
+    s.share = share;
+    s.cursor = share * blockIdx.x;
   }
   if (first && p.target > 0) {         // for the join kernel
-    if (tid == 0) p.plan[0] = chunk;
-    int at = slots - mine_s;
+    if (tid == 0) p.plan[0] = share;
+    long long at = sum - mine;
     for (int b = b0; b < b1; ++b) {
       const SeqWork w = seq_work(p, b, false);
-      const int sp = splits_of(w.units, chunk);
-      p.plan[kAttnPlanHead + b] = at;
-      if (sp > 1) at += w.tiles * p.kvh * sp;
+      p.plan[1 + b] = at;
+      at += (long long)w.tiles * p.kvh * w.units;
     }
   }
   __syncthreads();
 }
 
-// Calls take(b, work, local, splits, slot) on the one thread whose sequences
-// hold item c (on none if the lengths changed under the call).
+// One CTA's part of one item: rows of a tile, one key/value head, blocks of keys.
+struct AttnPiece {
+  int b, c0, head;
+  int slot;                            // where the sums go, or -1: the item is whole
+  int row0, nrows;                     // rows of the sequence
+  int past;                            // tokens before the new ones (may be negative)
+  int kv_end;                          // keys that the last row sees
+  int blk0, blk1;
+};
+
+// Units x0 .. x1 of item `local` of a sequence.  Late tiles see the most keys,
+// so they come first.
+__device__ __forceinline__ AttnPiece piece_of(const AttnParams& p, int b, const SeqWork& w,
+                                              int local, int x0, int x1, int slot) {
+  AttnPiece q;
+  const int up = local / p.kvh;
+  q.b = b;
+  q.c0 = w.c0;
+  q.head = local - up * p.kvh;
+  q.slot = slot;
+  q.row0 = (w.tiles - 1 - up) << p.rt_shift;
+  q.nrows = min(1 << p.rt_shift, w.n * p.G - q.row0);
+  q.past = w.len - w.n;
+  q.kv_end = max(0, q.past + (q.row0 + q.nrows - 1) / p.G + 1);
+  const int blocks = (q.kv_end + (1 << p.unit_shift) - 1) >> p.unit_shift;
+  q.blk0 = x0 == 0 ? 0 : (int)((long long)blocks * x0 / w.units);
+  q.blk1 = x1 == w.units ? blocks : (int)((long long)blocks * x1 / w.units);
+  return q;
+}
+
+// Whole item c: calls take(piece) on the one thread whose sequences hold it
+// (on none if the lengths changed under the call).
 template <class F>
-__device__ __forceinline__ void find_item_as(const AttnParams& p, const PlanShared& s, int c,
-                                             F&& take) {
+__device__ __forceinline__ void find_item(const AttnParams& p, const PlanShared& s, long long c,
+                                          F&& take) {
   const int tid = threadIdx.x;
-  if (tid >= kAttnThreads || c < s.items[tid] || c >= s.items[tid + 1]) return;
+  if (tid >= kAttnThreads || c < s.first[tid] || c >= s.first[tid + 1]) return;
   const int per = (p.pb.batch + kAttnThreads - 1) / kAttnThreads;
-  const int b1 = min(p.pb.batch, (tid + 1) * per);
-  int at = s.items[tid], slot = s.slots[tid];
-  for (int b = tid * per; b < b1; ++b) {
+  long long at = s.first[tid];
+  for (int b = tid * per; b < p.pb.batch; ++b) {
     const SeqWork w = seq_work(p, b, false);
-    const int sp = splits_of(w.units, s.chunk);
-    const int k = w.tiles * p.kvh * sp;
+    const long long k = (long long)w.tiles * p.kvh;
     if (c < at + k) {
-      take(b, w, c - at, sp, sp > 1 ? slot + (c - at) : -1);
+      take(piece_of(p, b, w, (int)(c - at), 0, 1, -1));
       return;
     }
     at += k;
-    if (sp > 1) slot += k;
   }
 }
 
-// Sequence of item c, and its place there, in the plan.  All threads of the CTA.
-__device__ __forceinline__ void find_item(const AttnParams& p, PlanShared& s, int c) {
-  if (threadIdx.x == 0) s.b = -1;
-  __syncthreads();
-  find_item_as(p, s, c, [&](int b, const SeqWork& w, int local, int splits, int slot) {
-    s.b = b;
-    s.w = w;
-    s.local = local;
-    s.splits = splits;
-    s.slot = slot;
-  });
-  __syncthreads();
-}
-
-// Item `local` of a sequence: its tile, key/value head and split.  Late tiles
-// see the most keys, so they come first.
-__device__ __forceinline__ void item_place(const AttnParams& p, const SeqWork& w, int local,
-                                           int splits, int& tile, int& head, int& split) {
-  split = local % splits;
-  const int i = local / splits;
-  head = i % p.kvh;
-  tile = w.tiles - 1 - i / p.kvh;
+// The next pieces of this CTA's share, `most` at most: take(k, piece) for each
+// and put their number in `count` (shared), on one thread; the cursor moves
+// on.  All threads call it, and a barrier follows.
+template <class F>
+__device__ __forceinline__ void next_pieces(const AttnParams& p, PlanShared& s, int most,
+                                            int& count, F&& take) {
+  const int tid = threadIdx.x;
+  const long long begin = s.share * blockIdx.x;
+  const long long end = min(begin + s.share, s.total);
+  long long pos = s.cursor;
+  __syncthreads();                     // every thread has it before one moves it on
+  if (pos >= end) {
+    if (tid == 0) count = 0;
+    return;
+  }
+  if (tid >= kAttnThreads || pos < s.first[tid] || pos >= s.first[tid + 1]) return;
+  const int per = (p.pb.batch + kAttnThreads - 1) / kAttnThreads;
+  long long at = s.first[tid];
+  int k = 0;
+  for (int b = tid * per; b < p.pb.batch && k < most && pos < end; ++b) {
+    const SeqWork w = seq_work(p, b, false);
+    const long long all = (long long)w.tiles * p.kvh * w.units;
+    while (pos < at + all && k < most && pos < end) {
+      const int local = (int)((pos - at) / w.units);
+      const long long item = at + (long long)local * w.units;
+      const int x0 = (int)(pos - item);
+      const int x1 = (int)min((long long)w.units, end - item);
+      const int slot =
+          x0 == 0 && x1 == w.units ? -1 : 2 * (int)blockIdx.x + (x0 == 0 ? 1 : 0);
+      take(k++, piece_of(p, b, w, local, x0, x1, slot));
+      pos = item + x1;
+    }
+    at += all;
+  }
+  count = k;
+  s.cursor = k > 0 ? pos : end;
 }
 
 // ------------------------------------------------------------ instructions
@@ -285,6 +294,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
   using C = AttnConfig<DP, WR, F32>;
   extern __shared__ __align__(1024) uint8_t attn_smem[];
   __shared__ PlanShared plan;
+  __shared__ AttnPiece s_piece;
+  __shared__ int s_count;
   __shared__ float s_m[4][16], s_l[4][16];
   const uint32_t sq = smem_u32(attn_smem), skv = sq + C::OFF_KV;
   long long* s_off = reinterpret_cast<long long*>(attn_smem + C::OFF_PAGES);
@@ -296,25 +307,26 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
   grid_dependency_wait();
   make_plan(p, plan);
 
-  for (int c = blockIdx.x; c < plan.total; c += gridDim.x) {
-    find_item(p, plan, c);
-    const SeqWork w = plan.w;
-    const int splits = plan.splits, slot = plan.slot, b = plan.b;
-    if (b < 0) {
+  for (long long c = blockIdx.x;; c += gridDim.x) {
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    if (p.target > 0)
+      next_pieces(p, plan, 1, s_count, [&](int, const AttnPiece& q) { s_piece = q; });
+    else if (c < plan.total)
+      find_item(p, plan, c, [&](const AttnPiece& q) {
+        s_piece = q;
+        s_count = 1;
+      });
+    __syncthreads();
+    if (s_count == 0) {
+      if (p.target > 0 || c + gridDim.x >= plan.total) break;
       __syncthreads();
       continue;
     }
-    int tile, head, split;
-    item_place(p, w, plan.local, splits, tile, head, split);
-    const int rows = w.n * p.G;                      // of the whole sequence
-    const int row0 = tile * C::RT;
-    const int nrows = min(C::RT, rows - row0);
-    const int past = w.len - w.n;                    // tokens before the new ones (may be < 0)
-    const int kv_end = max(0, past + (row0 + nrows - 1) / p.G + 1);
+    const int b = s_piece.b, c0 = s_piece.c0, head = s_piece.head, slot = s_piece.slot;
+    const int row0 = s_piece.row0, nrows = s_piece.nrows, past = s_piece.past;
+    const int kv_end = s_piece.kv_end, blk0 = s_piece.blk0, blk1 = s_piece.blk1;
     const int lim_first = past + row0 / p.G + 1;     // keys that the first row sees
-    const int blocks = (kv_end + kAttnTile - 1) / kAttnTile;
-    const int blk0 = (int)((long long)blocks * split / splits);
-    const int blk1 = (int)((long long)blocks * (split + 1) / splits);
 
     // ---- queries to shared memory (zeros past the rows and past D)
     for (int i = tid; i < C::RT * (DP / 8); i += kAttnThreads) {
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
       const bool ok = r < nrows && ch < chunks;
       const int rr = row0 + (ok ? r : 0);
       const long long off =
-          ((long long)(w.c0 + rr / p.G) * p.qh + (long long)head * p.G + rr % p.G) * D + 8 * ch;
+          ((long long)(c0 + rr / p.G) * p.qh + (long long)head * p.G + rr % p.G) * D + 8 * ch;
       uint4 u[C::TERMS];
 #pragma unroll
       for (int t = 0; t < C::TERMS; ++t) u[t] = make_uint4(0, 0, 0, 0);
@@ -530,7 +542,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
       }
       const int rr = row0 + r;
       const long long off =
-          ((long long)(w.c0 + rr / p.G) * p.qh + (long long)head * p.G + rr % p.G) * D + d;
+          ((long long)(c0 + rr / p.G) * p.qh + (long long)head * p.G + rr % p.G) * D + d;
       if constexpr (F32)
         *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.O) + off) = make_float2(x, y);
       else
@@ -612,9 +624,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
 }
 
 // --------------------------------------------------------------- the join
-// One CTA per token row and query head.  Its split count comes from the
-// lengths and the blocks per split that the attention kernel left in the
-// plan; warps take the splits in turn, lanes the D values.
+// One CTA per token row and query head.  The shares that hold parts of its
+// item follow from the item's place on the line of units and the share that
+// the attention kernel left in the plan: the first one wrote slot 2 s + 1, the
+// others slot 2 s.  Warps take the parts in turn, lanes the D values.
 template <bool F32>
 __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
   __shared__ float s_o[4][kRopeMaxDim];
@@ -627,26 +640,29 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
   if (b >= p.pb.batch) return;
   const SeqWork w = seq_work(p, b, false);
   if (w.n == 0 || r < w.c0) return;
-  const int splits = splits_of(w.units, p.plan[0]);
-  if (splits == 1) return;
+  const int RT = 1 << p.rt_shift;
   const int head = qhead / p.G;
   const int row = (r - w.c0) * p.G + qhead % p.G;
-  const int tile = row / p.RT, rt = row % p.RT;
-  const long long slot0 = (long long)p.plan[kAttnPlanHead + b] +
-                          ((long long)(w.tiles - 1 - tile) * p.kvh + head) * splits;
-  const long long size = (long long)p.RT * (p.D + 2);
-  const float* part = p.part + slot0 * size;
+  const int rt = row & (RT - 1);
+  const long long share = p.plan[0];
+  const long long item =
+      p.plan[1 + b] + ((long long)(w.tiles - 1 - (row >> p.rt_shift)) * p.kvh + head) * w.units;
+  const int first = (int)(item / share);
+  const int splits = (int)((item + w.units - 1) / share) - first + 1;
+  if (splits == 1) return;
+  const long long size = (long long)RT * (p.D + 2);
+  auto part = [&](int s) { return p.part + (2ll * (first + s) + (s == 0 ? 1 : 0)) * size; };
   const int per = p.D / 8;                           // 8 values per lane, up to 32 lanes
   float m = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int s = warp; s < splits; s += 4) m = fmaxf(m, part[s * size + rt]);
+  for (int s = warp; s < splits; s += 4) m = fmaxf(m, part(s)[rt]);
   if (m != -INFINITY) {
 #pragma unroll 4
     for (int s = warp; s < splits; s += 4) {
-      const float* q = part + s * size;
+      const float* q = part(s);
       const float f = ex2(q[rt] - m);
-      l += f * q[p.RT + rt];
+      l += f * q[RT + rt];
       if (lane < per) {
-        const float4* v = reinterpret_cast<const float4*>(q + 2 * p.RT + rt * p.D + 8 * lane);
+        const float4* v = reinterpret_cast<const float4*>(q + 2 * RT + rt * p.D + 8 * lane);
         const float4 x = v[0], y = v[1];
         o[0] += f * x.x; o[1] += f * x.y; o[2] += f * x.z; o[3] += f * x.w;
         o[4] += f * y.x; o[5] += f * y.y; o[6] += f * y.z; o[7] += f * y.w;

@@ -150,7 +150,7 @@ __device__ __forceinline__ void ex2_poly2(uint64_t z, float& x, float& y) {
 }
 
 constexpr int kAttnTcThreads = 384;
-constexpr int kAttnTcTarget = 148;     // splits wanted: one per SM
+constexpr int kAttnTcTarget = 148;     // most shares of a call: one per SM
 constexpr int kAttnTcKeys = 128;       // keys per block
 constexpr int kAttnTcPoly = 4;         // every fourth pair of powers on the fp32 pipe
 constexpr float kAttnTcLazy = 8.0f;    // growth of a row's maximum that rescales O
@@ -158,8 +158,8 @@ constexpr float kAttnTcLazy = 8.0f;    // growth of a row's maximum that rescale
 constexpr int kAttnTcList = 8;         // items laid out at a time
 
 struct AttnTcItem {
-  int b, c0, head, slot, row0, nrows, past, kv_end;
-  int blk0, count, tail, fix;          // blocks blk0 .. blk0 + count - 1; count < 0: no item
+  AttnPiece q;
+  int count, tail, fix;                // blocks; count < 0: no item
   int cnt[2];                          // blocks of each tile
 };
 
@@ -176,7 +176,7 @@ struct AttnTcConfig {
   static constexpr int OFF_PLAN = OFF_BAR + NUM_BARS * 8 + 16;
   static constexpr int OFF_ITEMS = OFF_PLAN + (int)((sizeof(PlanShared) + 15) & ~15u);
   static constexpr int SMEM =
-      OFF_ITEMS + kAttnTcList * (int)sizeof(AttnTcItem) + 1024;            // + alignment slack
+      OFF_ITEMS + kAttnTcList * (int)sizeof(AttnTcItem) + 16 + 1024;            // + alignment slack
   static constexpr uint32_t S_COL = 0, O_COL = 256;          // + 128 T
   static_assert(OFF_PLAN % 16 == 0 && SMEM <= 227 * 1024, "shared memory");
 };
@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   PlanShared& plan = *reinterpret_cast<PlanShared*>(smem + C::OFF_PLAN);
   AttnTcItem* items = reinterpret_cast<AttnTcItem*>(smem + C::OFF_ITEMS);
+  int* listed = reinterpret_cast<int*>(items + kAttnTcList);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int D = p.D;
 
@@ -246,46 +247,41 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
   // are all that ties them, so the producer fetches the next item's keys while
   // the softmax still writes the last one's rows.  Only the list of items is
   // common, laid out kAttnTcList at a time.
+  auto lay_out = [&](int k, const AttnPiece& q) {
+    AttnTcItem& job = items[k];
+    job.q = q;
+    // tile 0 ends with the keys its last row sees
+    const int last0 = q.row0 + min(q.nrows, 128) - 1;
+    const int end0 = (max(0, q.past + last0 / p.G + 1) + kAttnTcKeys - 1) / kAttnTcKeys;
+    job.cnt[0] = max(0, min(q.blk1, end0) - q.blk0);
+    job.cnt[1] = q.nrows > 128 ? q.blk1 - q.blk0 : 0;
+    job.count = max(job.cnt[0], job.cnt[1]);
+    // the block that holds the last key needs its value rows past it zeroed
+    job.tail = q.kv_end - (q.blk0 + job.count - 1) * kAttnTcKeys;
+    job.fix = job.count > 0 && job.tail < kAttnTcKeys;
+  };
   auto walk = [&](auto&& role) {
-    for (int wave = 0; (long long)wave * gridDim.x < plan.total; wave += kAttnTcList) {
+    for (long long wave = 0;; wave += kAttnTcList) {
       __syncthreads();                           // the last list is done with
       if (threadIdx.x < kAttnTcList) items[threadIdx.x].count = -1;
+      if (threadIdx.x == 0) *listed = 0;
       __syncthreads();
-      for (int k = 0; k < kAttnTcList; ++k) {
-        // items come longest first: every other wave runs the other way round,
-        // so that a CTA's share evens out
-        const int at = ((wave + k) & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
-        const long long c = (long long)(wave + k) * gridDim.x + at;
-        AttnTcItem& job = items[k];
-        if (c < plan.total)
-          find_item_as(p, plan, (int)c, [&](int b, const SeqWork& w, int local, int splits,
-                                            int slot) {
-            int tile, split;
-            item_place(p, w, local, splits, tile, job.head, split);
-            job.b = b;
-            job.c0 = w.c0;
-            job.slot = slot;
-            job.row0 = tile * C::RT;
-            job.nrows = min(C::RT, w.n * p.G - job.row0);
-            job.past = w.len - w.n;
-            job.kv_end = max(0, job.past + (job.row0 + job.nrows - 1) / p.G + 1);
-            const int blocks = (job.kv_end + kAttnTcKeys - 1) / kAttnTcKeys;
-            job.blk0 = (int)((long long)blocks * split / splits);
-            const int blk1 = (int)((long long)blocks * (split + 1) / splits);
-            // tile 0 ends with the keys its last row sees
-            const int last0 = job.row0 + min(job.nrows, 128) - 1;
-            const int end0 =
-                (max(0, job.past + last0 / p.G + 1) + kAttnTcKeys - 1) / kAttnTcKeys;
-            job.cnt[0] = max(0, min(blk1, end0) - job.blk0);
-            job.cnt[1] = job.nrows > 128 ? blk1 - job.blk0 : 0;
-            job.count = max(job.cnt[0], job.cnt[1]);
-            // the block that holds the last key needs its value rows past it zeroed
-            job.tail = job.kv_end - (job.blk0 + job.count - 1) * kAttnTcKeys;
-            job.fix = job.count > 0 && job.tail < kAttnTcKeys;
-          });
+      if (p.target > 0) {
+        next_pieces(p, plan, kAttnTcList, *listed, lay_out);
+      } else {
+        for (int k = 0; k < kAttnTcList; ++k) {
+          // items come longest first: every other wave runs the other way
+          // round, so that a CTA's share evens out
+          const int at = ((wave + k) & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+          const long long c = (wave + k) * gridDim.x + at;
+          if (c < plan.total) find_item(p, plan, c, [&](const AttnPiece& q) { lay_out(k, q); });
+        }
+        if (threadIdx.x == 0) *listed = wave * gridDim.x < plan.total ? kAttnTcList : 0;
       }
       __syncthreads();
-      for (int k = 0; k < kAttnTcList; ++k) {
+      const int n = *listed;
+      if (n == 0) break;
+      for (int k = 0; k < n; ++k) {
         const AttnTcItem job = items[k];
         if (job.count < 0) continue;
         role(job);
@@ -307,21 +303,21 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       // --------------------------------------------------------- softmax
       const int t = warp >> 2, r = threadIdx.x & 127;        // tile and row in it
       const int row = 128 * t + r;                           // of the item
-      const bool live = row < job.nrows;
+      const bool live = row < job.q.nrows;
       // Rows move 16 bytes a lane, so that a warp takes whole rows at a time:
       // LR lanes per row, rows sub, sub + 32 / LR, ... of the warp's 32.
       constexpr int LR = DP / 8, STEP = 32 / LR;
       const int ch = lane % LR, sub = lane / LR, wrow = 32 * (warp & 3);
       uint8_t* qtile = smem + t * C::TILE + (ch >> 3) * C::SUB;
       // element offset of the first such row, and the way to the next
-      const int gr0 = job.row0 + 128 * t + wrow + sub;
+      const int gr0 = job.q.row0 + 128 * t + wrow + sub;
       const int tok0 = gr0 / p.G, g0 = gr0 - tok0 * p.G;
       const int tok_step = STEP / p.G, g_step = STEP - tok_step * p.G;
       auto each_row = [&](auto&& f) {
         int tok = tok0, g = g0;
 #pragma unroll
         for (int k = 0; k < LR; ++k) {
-          f(k, ((long long)(job.c0 + tok) * p.qh + (long long)job.head * p.G + g) * D + 8 * ch);
+          f(k, ((long long)(job.q.c0 + tok) * p.qh + (long long)job.q.head * p.G + g) * D + 8 * ch);
           tok += tok_step;
           g += g_step;
           if (g >= p.G) {
@@ -334,7 +330,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         uint4 u[LR];
         each_row([&](int k, long long off) {
           u[k] = make_uint4(0, 0, 0, 0);
-          if (128 * t + wrow + sub + STEP * k < job.nrows && 8 * ch < D)
+          if (128 * t + wrow + sub + STEP * k < job.q.nrows && 8 * ch < D)
             u[k] = *reinterpret_cast<const uint4*>(
                 reinterpret_cast<const __nv_bfloat16*>(p.Q) + off);
         });
@@ -350,7 +346,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       const uint32_t lanes = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
       const uint32_t scol = lanes + C::S_COL + 128u * t, ocol = lanes + C::O_COL + 128u * t;
       // keys this row sees
-      const int lim = live ? job.past + (job.row0 + row) / p.G + 1 : 0;
+      const int lim = live ? job.q.past + (job.q.row0 + row) / p.G + 1 : 0;
       // keys that the warp's rows all see
       const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
       float m = -INFINITY;                                   // reference, log2 units
@@ -367,7 +363,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(scol + 32u * q, s[q]);
         tmem_ld_wait();
-        const int key0 = (job.blk0 + i) * kAttnTcKeys;
+        const int key0 = (job.q.blk0 + i) * kAttnTcKeys;
         const bool masked = key0 + kAttnTcKeys > lim_warp;
         if (masked) {
           const int n = lim - key0;
@@ -463,10 +459,10 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       if (ok && job.cnt[t] > 0)
         ok = mbar_wait(&odone[t], (blocks_done[t] + job.cnt[t] - 1) & 1u, abort_flag);
       tc_fence_after();
-      if (ok && 128 * t < job.nrows) {
-        float* part = job.slot >= 0 ? p.part + (long long)job.slot * C::RT * (D + 2) : nullptr;
-        const float inv = job.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
-        if (job.slot >= 0 && live) {
+      if (ok && 128 * t < job.q.nrows) {
+        float* part = job.q.slot >= 0 ? p.part + (long long)job.q.slot * C::RT * (D + 2) : nullptr;
+        const float inv = job.q.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+        if (job.q.slot >= 0 && live) {
           part[row] = m;
           part[C::RT + row] = l;
         }
@@ -485,7 +481,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[k + e]) * inv;
-            if (job.slot >= 0) {
+            if (job.q.slot >= 0) {
               if (live && d + k < D) store_f32<8>(part + 2 * C::RT + (long long)row * D + d + k, x);
             } else {                             // through the Q tile, which is done with
               store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(
@@ -494,11 +490,11 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
             }
           }
         }
-        if (job.slot < 0) {
+        if (job.q.slot < 0) {
           __syncwarp();
           each_row([&](int k, long long off) {
             const int rr = wrow + sub + STEP * k;
-            if (128 * t + rr < job.nrows && 8 * ch < D)
+            if (128 * t + rr < job.q.nrows && 8 * ch < D)
               *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.O) + off) =
                   *reinterpret_cast<const uint4*>(qtile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
           });
@@ -516,13 +512,13 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       bool ok = true;
       for (int i = 0; i < 2 * job.count; ++i) {
         const uint32_t it = slot_it + i;
-        const int key0 = (job.blk0 + (i >> 1)) * kAttnTcKeys;
+        const int key0 = (job.q.blk0 + (i >> 1)) * kAttnTcKeys;
         // lane x < pieces: place of piece x (out of range: the load fills zeros)
         const int key = key0 + lane * box_rows;
-        const bool live = lane < pieces && key < job.kv_end;
+        const bool live = lane < pieces && key < job.q.kv_end;
         int page = -1;
         if (live) {
-          page = __ldg(p.pb.table + (long long)job.b * p.pb.stride + key / p.pb.page_size);
+          page = __ldg(p.pb.table + (long long)job.q.b * p.pb.stride + key / p.pb.page_size);
           if (page < 0 || page >= p.pb.num_pages) {
             record_device_error(DEV_ERR_INDEX);
             page = p.pb.num_pages;
@@ -541,7 +537,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
 #pragma unroll
           for (int h = 0; h < C::HALVES; ++h)
             tma_load_3d(dst + h * C::SUB, (i & 1) ? &tm_v : &tm_k, &full[st], 64 * h,
-                        key % p.pb.page_size, page * p.kvh + job.head);
+                        key % p.pb.page_size, page * p.kvh + job.q.head);
         }
       }
       });

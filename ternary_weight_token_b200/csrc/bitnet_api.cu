@@ -863,15 +863,15 @@ int validate_paged(int dtype, int M, int q_heads, int kv_heads, int head_dim, in
     return fail(BITNET_ERR_INVALID_ARG, "table_stride * page_size must be at most 2^30");
   if ((long long)num_pages * kv_heads > 0x7fffffffll)
     return fail(BITNET_ERR_INVALID_ARG, "num_pages * kv_heads must be below 2^31");
-  if ((long long)M * q_heads > 0x7fffffffll)
-    return fail(BITNET_ERR_INVALID_ARG, "M * q_heads must be below 2^31");
+  if ((long long)M * q_heads > (1ll << 30))
+    return fail(BITNET_ERR_INVALID_ARG, "M * q_heads must be at most 2^30");
   return BITNET_OK;
 }
 
-// Row tile and split target of an attention call (pure host logic).
+// Kernel and row tile of an attention call (pure host logic).
 struct AttnShape {
   bool tc;                             // tensor-core kernel
-  int RT, unit, min_units, target;
+  int rt_shift, unit_shift, min_units, target;
 };
 
 AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, bool f32,
@@ -885,18 +885,18 @@ AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, 
   const bool few = (long long)M * G <= 16ll * batch;
   sh.tc = !few && !f32 && head_dim <= 128 && scale > 0.0f;
   if (sh.tc) {
-    sh.RT = 256;
-    sh.unit = kAttnTcKeys;
-    sh.min_units = 2;
+    sh.rt_shift = 8;
+    sh.unit_shift = 7;
+    sh.min_units = 3;
     sh.target = kAttnTcTarget;
   } else {
-    sh.RT = few || head_dim > 128 ? 16 : 64;
-    sh.unit = kAttnTile;
-    sh.min_units = 4;
+    sh.rt_shift = few || head_dim > 128 ? 4 : 6;
+    sh.unit_shift = 6;
+    sh.min_units = 5;
     sh.target = kAttnTarget;
   }
-  // enough items without splitting
-  if ((long long)M * G / sh.RT * kv_heads >= 2 * sh.target) sh.target = 0;
+  // enough items to deal out whole
+  if (((long long)M * G >> sh.rt_shift) * kv_heads >= 2 * sh.target) sh.target = 0;
   return sh;
 }
 
@@ -920,9 +920,11 @@ int launch_attn_tc(const AttnParams& p, int sms, cudaStream_t st) {
     return rc;
   auto kern = attn_tc_kernel<DP>;
   if (int rc = set_smem_attr((const void*)kern, C::SMEM)) return rc;
-  const long long items = ((long long)p.pb.M * p.G / C::RT + p.pb.batch) * p.kvh + p.target;
-  const int grid = (int)std::min<long long>(items, sms);
-  return launch_pdl(kern, dim3(grid), dim3(kAttnTcThreads), C::SMEM, st, mk, mv, p, box);
+  AttnParams q = p;
+  if (q.target > sms) q.target = sms;
+  const long long items = ((long long)p.pb.M * p.G / C::RT + p.pb.batch) * p.kvh;
+  const int grid = q.target > 0 ? q.target : (int)std::min<long long>(items, sms);
+  return launch_pdl(kern, dim3(grid), dim3(kAttnTcThreads), C::SMEM, st, mk, mv, q, box);
 }
 
 template <int DP, int WR, bool F32>
@@ -932,10 +934,12 @@ int launch_attn_rows(const AttnParams& p, int sms, cudaStream_t st) {
   if (int rc = set_smem_attr((const void*)kern, C::SMEM)) return rc;
   int per_sm = 0;
   if (int rc = occupancy(per_sm, (const void*)kern, kAttnThreads, C::SMEM)) return rc;
-  const long long items =
-      ((long long)p.pb.M * p.G / C::RT + p.pb.batch) * p.kvh + p.target;   // at most
-  const long long cap = (long long)sms * (per_sm < 1 ? 1 : per_sm);
-  return launch_pdl(kern, dim3((unsigned)std::min(items, cap)), dim3(kAttnThreads), C::SMEM, st, p);
+  AttnParams q = p;
+  const int cap = sms * (per_sm < 1 ? 1 : per_sm);
+  if (q.target > cap) q.target = cap;
+  const long long items = ((long long)p.pb.M * p.G / C::RT + p.pb.batch) * p.kvh;   // at most
+  const int grid = q.target > 0 ? q.target : (int)std::min<long long>(items, cap);
+  return launch_pdl(kern, dim3(grid), dim3(kAttnThreads), C::SMEM, st, q);
 }
 
 template <int WR, bool F32>
@@ -1580,7 +1584,7 @@ size_t bitnet_attention_workspace_size(int M, int batch, int q_heads, int kv_hea
   // (the split slots of tiles of 64 and of 256 rows take the same room)
   static_assert(kAttnTarget * 64 >= kAttnTcTarget * 256, "split slots");
   const int rt = (long long)M * (q_heads / kv_heads) <= 16 || head_dim > 128 ? 16 : 64;
-  return align256(((size_t)batch + kAttnPlanHead) * 4) +
+  return align256(((size_t)batch + 1) * 8) +
          (size_t)2 * kAttnTarget * rt * (head_dim + 2) * 4;
 }
 
@@ -1620,17 +1624,18 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   p.Vc = reinterpret_cast<const __nv_bfloat16*>(v_cache);
   p.qh = q_heads; p.kvh = kv_heads; p.G = q_heads / kv_heads; p.D = head_dim;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  p.RT = sh.RT; p.unit = sh.unit; p.min_units = sh.min_units; p.target = sh.target;
-  // sequences that cannot hold more than one split never need the join
-  if ((long long)table_stride * page_size <= (long long)sh.min_units * sh.unit) p.target = 0;
-  p.plan = reinterpret_cast<int*>(workspace);
+  p.rt_shift = sh.rt_shift; p.unit_shift = sh.unit_shift;
+  p.min_units = sh.min_units; p.target = sh.target;
+  // sequences shorter than the smallest share are not worth cutting
+  if ((long long)table_stride * page_size < (long long)sh.min_units << sh.unit_shift) p.target = 0;
+  p.plan = reinterpret_cast<long long*>(workspace);
   p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
-                                    align256(((size_t)batch + kAttnPlanHead) * 4));
+                                    align256(((size_t)batch + 1) * 8));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int rc;
   if (sh.tc)
     rc = head_dim <= 64 ? launch_attn_tc<64>(p, di.sms, st) : launch_attn_tc<128>(p, di.sms, st);
-  else if (sh.RT == 16)
+  else if (sh.rt_shift == 4)
     rc = f32 ? launch_attn_dim<1, true>(p, di.sms, st) : launch_attn_dim<1, false>(p, di.sms, st);
   else
     rc = f32 ? launch_attn_dim<4, true>(p, di.sms, st) : launch_attn_dim<4, false>(p, di.sms, st);
