@@ -33,6 +33,7 @@ namespace bitnet {
 
 constexpr int kAttnThreads = 128;
 constexpr int kAttnTile = 64;          // keys per block of the mma.sync kernel
+constexpr int kAttnPlanHead = 2;       // words of the plan before the sequences'
 constexpr int kAttnTarget = 592;       // most shares of a call (mma.sync kernel)
 
 struct AttnParams {
@@ -45,7 +46,7 @@ struct AttnParams {
   int rt_shift, unit_shift;            // log2 of the rows per tile and the keys per block
   int min_units;                       // smallest share
   int target;                          // shares wanted, 0: whole items, dealt out in turn
-  long long* plan;                     // [0] units per share, [1 + b] units before sequence b
+  long long* plan;                     // units per share, alignment; units before each sequence
   float* part;                         // slots: m[RT], l[RT], o[RT][D]
 };
 
@@ -55,7 +56,8 @@ struct SeqWork {
   int tiles, units;                    // row tiles; units of one item
 };
 
-__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool report) {
+// align > 0: items are rounded up to whole shares of that many units.
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool report, int align) {
   SeqWork w;
   w.c0 = __ldg(p.pb.cu_q + b);
   const int c1 = __ldg(p.pb.cu_q + b + 1);
@@ -73,13 +75,18 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool rep
     w.len = w.len < 0 ? 0 : cap;
   }
   w.tiles = (w.n * p.G + (1 << p.rt_shift) - 1) >> p.rt_shift;
-  w.units = p.target > 0 ? ((w.len + (1 << p.unit_shift) - 1) >> p.unit_shift) + 1 : 1;
+  w.units = 1;
+  if (p.target > 0) {
+    const int blocks = (w.len + (1 << p.unit_shift) - 1) >> p.unit_shift;
+    w.units = align > 0 ? max((blocks + align - 1) / align, 1) * align : blocks + 1;
+  }
   return w;
 }
 
 // Thread t of the CTA holds sequences [t per, (t + 1) per) of the batch.
 struct PlanShared {
   long long share, total;              // units per share, of the call
+  int align;                           // items are whole shares of that many units, or 0
   long long cursor;                    // where this CTA's share goes on
   long long first[kAttnThreads + 1];   // units before each thread's sequences
   long long red[kAttnThreads / 32];
@@ -92,41 +99,47 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
   const int per = (B + kAttnThreads - 1) / kAttnThreads;
   const int b0 = tid * per, b1 = min(B, b0 + per);
   const bool first = blockIdx.x == 0;
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const SeqWork w = seq_work(p, b, first);
-    mine += (long long)w.tiles * p.kvh * w.units;
+  // smallest shares first; if those are too many, equal ones
+  int align = p.target > 0 ? p.min_units : 0;
+  long long share = max(align, 1), mine, sum, total;
+  for (;;) {
+    mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const SeqWork w = seq_work(p, b, first, align);
+      mine += (long long)w.tiles * p.kvh * w.units;
+    }
+    sum = mine;                        // inclusive scan
+    for (int o = 1; o < 32; o *= 2) {
+      const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    if (lane == 31 && warp < kAttnThreads / 32) s.red[warp] = sum;
+    __syncthreads();
+    for (int i = 0; i < warp && i < kAttnThreads / 32; ++i) sum += s.red[i];
+    total = 0;
+    for (int i = 0; i < kAttnThreads / 32; ++i) total += s.red[i];
+    if (align == 0 || total <= share * p.target) break;
+    align = 0;
+    __syncthreads();
   }
-  long long sum = mine;                // inclusive scan
-  for (int o = 1; o < 32; o *= 2) {
-    const long long x = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += x;
-  }
-  if (lane == 31 && warp < kAttnThreads / 32) s.red[warp] = sum;
-  __syncthreads();
-  for (int i = 0; i < warp && i < kAttnThreads / 32; ++i) sum += s.red[i];
+  if (p.target > 0 && align == 0) share = max((total + p.target - 1) / p.target, 1ll);
   if (tid < kAttnThreads) s.first[tid] = sum - mine;
-  long long total = 0;
-  for (int i = 0; i < kAttnThreads / 32; ++i) total += s.red[i];
-  long long share = 1;
-  if (p.target > 0) {
-    long long shares = total / p.min_units;
-    shares = shares < 1 ? 1 : shares > p.target ? p.target : shares;
-    share = (total + shares - 1) / shares;
-    if (share < 1) share = 1;
-  }
   if (tid == 0) {
     s.first[kAttnThreads] = total;
     s.total = total;
     s.share = share;
+    s.align = align;
     s.cursor = share * blockIdx.x;
   }
   if (first && p.target > 0) {         // for the join kernel
-    if (tid == 0) p.plan[0] = share;
+    if (tid == 0) {
+      p.plan[0] = share;
+      p.plan[1] = align;
+    }
     long long at = sum - mine;
     for (int b = b0; b < b1; ++b) {
-      const SeqWork w = seq_work(p, b, false);
-      p.plan[1 + b] = at;
+      const SeqWork w = seq_work(p, b, false, align);
+      p.plan[kAttnPlanHead + b] = at;
       at += (long long)w.tiles * p.kvh * w.units;
     }
   }
@@ -173,7 +186,7 @@ __device__ __forceinline__ void find_item(const AttnParams& p, const PlanShared&
   const int per = (p.pb.batch + kAttnThreads - 1) / kAttnThreads;
   long long at = s.first[tid];
   for (int b = tid * per; b < p.pb.batch; ++b) {
-    const SeqWork w = seq_work(p, b, false);
+    const SeqWork w = seq_work(p, b, false, s.align);
     const long long k = (long long)w.tiles * p.kvh;
     if (c < at + k) {
       take(piece_of(p, b, w, (int)(c - at), 0, 1, -1));
@@ -203,7 +216,7 @@ __device__ __forceinline__ void next_pieces(const AttnParams& p, PlanShared& s, 
   long long at = s.first[tid];
   int k = 0;
   for (int b = tid * per; b < p.pb.batch && k < most && pos < end; ++b) {
-    const SeqWork w = seq_work(p, b, false);
+    const SeqWork w = seq_work(p, b, false, s.align);
     const long long all = (long long)w.tiles * p.kvh * w.units;
     while (pos < at + all && k < most && pos < end) {
       const int local = (int)((pos - at) / w.units);
@@ -370,10 +383,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
       const int blk = blk0 + i;
       if (i % C::PAGE_TILES == 0) {                  // page offsets of the next blocks
         __syncthreads();
-        for (int k = tid; k < C::PAGE_TILES * 4; k += kAttnThreads) {
+        const int need = 4 * min(C::PAGE_TILES, blk1 - blk);
+        for (int k = tid; k < need; k += kAttnThreads) {
           const int key = blk * kAttnTile + 16 * k;  // capacities stay below 2^30
           long long off = -1;
-          if (blk + k / 4 < blk1 && key < kv_end) {
+          if (key < kv_end) {
             const int page = __ldg(p.pb.table + (long long)b * p.pb.stride + key / p.pb.page_size);
             if (page < 0 || page >= p.pb.num_pages)
               record_device_error(DEV_ERR_INDEX);
@@ -636,38 +650,46 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
   grid_launch_dependents();
   grid_dependency_wait();
   const int r = blockIdx.x, qhead = blockIdx.y;
+  const long long share = p.plan[0];
+  const int align = (int)p.plan[1];
   const int b = sequence_of(p.pb, r, lane);
   if (b >= p.pb.batch) return;
-  const SeqWork w = seq_work(p, b, false);
+  const long long before = p.plan[kAttnPlanHead + b];
+  const SeqWork w = seq_work(p, b, false, align);
   if (w.n == 0 || r < w.c0) return;
   const int RT = 1 << p.rt_shift;
   const int head = qhead / p.G;
   const int row = (r - w.c0) * p.G + qhead % p.G;
   const int rt = row & (RT - 1);
-  const long long share = p.plan[0];
   const long long item =
-      p.plan[1 + b] + ((long long)(w.tiles - 1 - (row >> p.rt_shift)) * p.kvh + head) * w.units;
+      before + ((long long)(w.tiles - 1 - (row >> p.rt_shift)) * p.kvh + head) * w.units;
   const int first = (int)(item / share);
   const int splits = (int)((item + w.units - 1) / share) - first + 1;
   if (splits == 1) return;
   const long long size = (long long)RT * (p.D + 2);
   auto part = [&](int s) { return p.part + (2ll * (first + s) + (s == 0 ? 1 : 0)) * size; };
   const int per = p.D / 8;                           // 8 values per lane, up to 32 lanes
+  // one pass with a running maximum: a part's statistics and sums are loaded
+  // together, four parts in flight
   float m = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int s = warp; s < splits; s += 4) m = fmaxf(m, part(s)[rt]);
-  if (m != -INFINITY) {
 #pragma unroll 4
-    for (int s = warp; s < splits; s += 4) {
-      const float* q = part(s);
-      const float f = ex2(q[rt] - m);
-      l += f * q[RT + rt];
-      if (lane < per) {
-        const float4* v = reinterpret_cast<const float4*>(q + 2 * RT + rt * p.D + 8 * lane);
-        const float4 x = v[0], y = v[1];
-        o[0] += f * x.x; o[1] += f * x.y; o[2] += f * x.z; o[3] += f * x.w;
-        o[4] += f * y.x; o[5] += f * y.y; o[6] += f * y.z; o[7] += f * y.w;
-      }
+  for (int s = warp; s < splits; s += 4) {
+    const float* q = part(s);
+    const float ms = q[rt], ls = q[RT + rt];
+    float4 x = make_float4(0, 0, 0, 0), y = x;
+    if (lane < per) {
+      const float4* v = reinterpret_cast<const float4*>(q + 2 * RT + rt * p.D + 8 * lane);
+      x = v[0];
+      y = v[1];
     }
+    const float mm = fmaxf(m, ms), base = mm == -INFINITY ? 0.0f : mm;
+    const float f = ex2(m - base), g = ex2(ms - base);
+    m = mm;
+    l = l * f + ls * g;
+    o[0] = o[0] * f + x.x * g; o[1] = o[1] * f + x.y * g;
+    o[2] = o[2] * f + x.z * g; o[3] = o[3] * f + x.w * g;
+    o[4] = o[4] * f + y.x * g; o[5] = o[5] * f + y.y * g;
+    o[6] = o[6] * f + y.z * g; o[7] = o[7] * f + y.w * g;
   }
   if (lane == 0) {
     s_ml[warp][0] = m;

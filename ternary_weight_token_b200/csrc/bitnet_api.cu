@@ -892,7 +892,7 @@ AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, 
   } else {
     sh.rt_shift = few || head_dim > 128 ? 4 : 6;
     sh.unit_shift = 6;
-    sh.min_units = 5;
+    sh.min_units = sh.rt_shift == 4 ? 2 : 8;
     sh.target = kAttnTarget;
   }
   // enough items to deal out whole
@@ -1584,7 +1584,7 @@ size_t bitnet_attention_workspace_size(int M, int batch, int q_heads, int kv_hea
   // (the split slots of tiles of 64 and of 256 rows take the same room)
   static_assert(kAttnTarget * 64 >= kAttnTcTarget * 256, "split slots");
   const int rt = (long long)M * (q_heads / kv_heads) <= 16 || head_dim > 128 ? 16 : 64;
-  return align256(((size_t)batch + 1) * 8) +
+  return align256(((size_t)batch + kAttnPlanHead) * 8) +
          (size_t)2 * kAttnTarget * rt * (head_dim + 2) * 4;
 }
 
@@ -1630,7 +1630,7 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   if ((long long)table_stride * page_size < (long long)sh.min_units << sh.unit_shift) p.target = 0;
   p.plan = reinterpret_cast<long long*>(workspace);
   p.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
-                                    align256(((size_t)batch + 1) * 8));
+                                    align256(((size_t)batch + kAttnPlanHead) * 8));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int rc;
   if (sh.tc)
