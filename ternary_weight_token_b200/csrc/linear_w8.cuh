@@ -19,6 +19,8 @@
 // many tokens: the tensor cores.  The token tile follows M (16 .. 256).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "gemv.cuh"
 
@@ -67,6 +69,44 @@ struct W8Params {
   int tiles_n, num_tiles;
   int out_type, flags;
 };
+
+// One thread's CW outputs (one weight row, consecutive tokens) of a tile: at =
+// first element, stride = elements between tokens, the first `live` tokens
+// stored.  One instance per output type and epilogue, so that the unrolled
+// code stays small.
+template <int CW, int TYPE, bool SILU, bool RESID>
+__device__ __forceinline__ void w8_store(const uint32_t (&v)[CW], float wf, const float* tok,
+                                         void* Y, const void* resid, size_t at, size_t stride,
+                                         int live) {
+  if constexpr (TYPE == OUT_I32) {
+    int32_t* y = reinterpret_cast<int32_t*>(Y) + at;
+#pragma unroll
+    for (int j = 0; j < CW; ++j, y += stride)
+      if (j < live) *y = (int)v[j];
+  } else {
+    using T = typename std::conditional<TYPE == OUT_BF16, __nv_bfloat16, float>::type;
+    float r[CW];
+    if constexpr (RESID) {                       // independent loads first
+      const T* q = reinterpret_cast<const T*>(resid) + at;
+#pragma unroll
+      for (int j = 0; j < CW; ++j, q += stride) r[j] = j < live ? static_cast<float>(*q) : 0.0f;
+    }
+    T* y = reinterpret_cast<T*>(Y) + at;
+#pragma unroll
+    for (int j = 0; j < CW; ++j, y += stride) {
+      // the sum, two reciprocals, their product and the last product: 2^-24 each
+      float x = __fmul_rn(__int2float_rn((int)v[j]), __fmul_rn(wf, tok[j]));
+      if constexpr (SILU) x = silu_f32(x);
+      if constexpr (RESID) x = __fadd_rn(r[j], x);
+      if (j < live) {
+        if constexpr (TYPE == OUT_BF16)
+          *y = __float2bfloat16_rn(x);
+        else
+          *y = x;
+      }
+    }
+  }
+}
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
@@ -186,43 +226,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tmem_ld_32x32b_x32(lane_base + ab * C::BN + c, v);
         else
           tmem_ld_32x32b_x16(lane_base + ab * C::BN + c, v);
-        float r[CW];
-        const size_t at = (size_t)(m0 + c) * p.N + n;
-        if (p.flags & EPI_RESIDUAL) {            // independent loads before the sums are read
-#pragma unroll
-          for (int j = 0; j < CW; ++j) {
-            r[j] = 0.0f;
-            if (n_ok && m0 + c + j < p.M) {
-              const size_t i = at + (size_t)j * p.N;
-              r[j] = p.out_type == OUT_BF16
-                         ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.resid)[i])
-                         : reinterpret_cast<const float*>(p.resid)[i];
-            }
-          }
-        }
         tmem_ld_wait();
-        if (!n_ok) continue;
-        if (p.out_type == OUT_I32) {
-          int32_t* y = reinterpret_cast<int32_t*>(p.Y) + at;
-#pragma unroll
-          for (int j = 0; j < CW; ++j)
-            if (m0 + c + j < p.M) y[(size_t)j * p.N] = (int)v[j];
-          continue;
-        }
-#pragma unroll
-        for (int j = 0; j < CW; ++j) {
-          // three roundings of 2^-24 at most beside the sum's own
-          float y = __fmul_rn(__int2float_rn((int)v[j]), __fmul_rn(wf, tok[c + j]));
-          if (p.flags & EPI_SILU) y = silu_f32(y);
-          if (p.flags & EPI_RESIDUAL) y = __fadd_rn(r[j], y);
-          if (m0 + c + j < p.M) {
-            const size_t i = at + (size_t)j * p.N;
-            if (p.out_type == OUT_BF16)
-              reinterpret_cast<__nv_bfloat16*>(p.Y)[i] = __float2bfloat16_rn(y);
+        if (n_ok) {
+          const size_t at = (size_t)(m0 + c) * p.N + n;
+          const int live = min(CW, p.M - (m0 + c));
+          const bool silu = (p.flags & EPI_SILU) != 0, res = (p.flags & EPI_RESIDUAL) != 0;
+          auto store = [&](auto type, auto si, auto re) {
+            w8_store<CW, decltype(type)::value, decltype(si)::value, decltype(re)::value>(
+                v, wf, tok + c, p.Y, p.resid, at, (size_t)p.N, live);
+          };
+          auto pick = [&](auto type) {
+            if (silu && res)
+              store(type, std::true_type{}, std::true_type{});
+            else if (silu)
+              store(type, std::true_type{}, std::false_type{});
+            else if (res)
+              store(type, std::false_type{}, std::true_type{});
             else
-              reinterpret_cast<float*>(p.Y)[i] = y;
-          }
+              store(type, std::false_type{}, std::false_type{});
+          };
+          if (p.out_type == OUT_BF16)
+            pick(std::integral_constant<int, OUT_BF16>{});
+          else if (p.out_type == OUT_F32)
+            pick(std::integral_constant<int, OUT_F32>{});
+          else
+            store(std::integral_constant<int, OUT_I32>{}, std::false_type{}, std::false_type{});
         }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
