@@ -255,12 +255,7 @@ def alloc_block_tail_workspace(M, H, I, device="cuda"):
 
 # The serving calls check shapes, types and devices here (the C side sees only
 # pointers).  They run once per layer and token, so the checks are written to
-# cost little: one pass over the tensors, messages formed only on failure.
-
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
+# cost little: plain tests, messages formed only on failure.
 
 def _device_ptrs(names, tensors):
     """Addresses of contiguous tensors (None for None), all on the current CUDA device, where
@@ -277,33 +272,37 @@ def _device_ptrs(names, tensors):
             out.append(t.data_ptr())
         else:
             name = names.split()[len(out)]
-            _need(t.is_cuda, f"{name} must live on a CUDA device")
-            _need(t.get_device() == index, f"{name} is on {t.device}, not on the current device")
-            _need(False, f"{name} must be contiguous")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must live on a CUDA device")
+            if t.get_device() != index:
+                raise ValueError(f"{name} is on {t.device}, not on the current device")
+            raise ValueError(f"{name} must be contiguous")
     return out
 
 
-def _rows(name, t, width, dtype, device):
-    """Address and row stride of a matrix whose rows are contiguous."""
-    _need(t.dim() == 2 and t.dtype == dtype and t.shape[1] == width,
-          f"{name} must be [M][{width}] of {dtype}")
-    _need(t.get_device() == device, f"{name} must live on Q_out's device")
+def _row_stride(name, t, M, width, dtype, device):
+    """Row stride of an [M][width] matrix whose rows are contiguous."""
+    if t.shape != (M, width) or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be [{M}][{width}] of {dtype}, on Q_out's device")
     row, col = t.stride()
-    _need(col == 1 or width == 1, f"the rows of {name} must be contiguous")
-    return t.data_ptr(), (row if t.shape[0] > 1 else width)
+    if col != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return row if M > 1 else width
 
 
 def _paged(cu_q, kv_len, block_table, k_cache, v_cache):
     """(batch, table_stride, num_pages, kv_heads, page_size, head_dim) of a paged cache."""
-    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and
-          k_cache.dtype == torch.bfloat16 and v_cache.dtype == torch.bfloat16,
-          "k_cache and v_cache must be bf16 [num_pages][kv_heads][page_size][head_dim]")
+    if not (k_cache.dim() == 4 and k_cache.shape == v_cache.shape and
+            k_cache.dtype == torch.bfloat16 and v_cache.dtype == torch.bfloat16):
+        raise ValueError("k_cache and v_cache must be bf16 "
+                         "[num_pages][kv_heads][page_size][head_dim]")
+    if not kv_len.dtype == cu_q.dtype == block_table.dtype == torch.int32:
+        raise ValueError("cu_q, kv_len and block_table must be int32")
     batch = kv_len.numel()
-    _need(kv_len.dtype == cu_q.dtype == block_table.dtype == torch.int32,
-          "cu_q, kv_len and block_table must be int32")
-    _need(kv_len.dim() == 1 and cu_q.dim() == 1 and cu_q.numel() == batch + 1 and
-          block_table.dim() == 2 and block_table.shape[0] == batch,
-          "kv_len must be [batch], cu_q [batch + 1], block_table [batch][table_stride]")
+    if not (kv_len.dim() == 1 and cu_q.dim() == 1 and cu_q.numel() == batch + 1 and
+            block_table.dim() == 2 and block_table.shape[0] == batch):
+        raise ValueError("kv_len must be [batch], cu_q [batch + 1], "
+                         "block_table [batch][table_stride]")
     pages, heads, page, dim = k_cache.shape
     return batch, block_table.shape[1], pages, heads, page, dim
 
@@ -314,19 +313,23 @@ def bitnet_linear_w8(Xq, x_scale, Wq, w_scale, Y, silu=False, residual=None, epi
     and scales of both sides from bitnet_quant_act (see include/bitnet.h)."""
     xq, xs, wq, ws, y, res = _device_ptrs("Xq x_scale Wq w_scale Y residual",
                                           (Xq, x_scale, Wq, w_scale, Y, residual))
-    _need(Xq.dim() == 2 and Wq.dim() == 2 and Xq.dtype == Wq.dtype == torch.int8 and
-          Xq.shape[1] == Wq.shape[1], "Xq and Wq must be int8 [M][K] and [N][K]")
+    if not (Xq.dim() == 2 and Wq.dim() == 2 and Xq.dtype == Wq.dtype == torch.int8 and
+            Xq.shape[1] == Wq.shape[1]):
+        raise ValueError("Xq and Wq must be int8 [M][K] and [N][K]")
     (M, K), N = Xq.shape, Wq.shape[0]
-    _need(x_scale.dtype == w_scale.dtype == torch.float32 and x_scale.numel() == M and
-          w_scale.numel() == N, "x_scale and w_scale must be fp32 [M] and [N]")
-    _need(Y.shape == (M, N), "Y must be [M][N]")
-    _need(residual is None or (residual.shape == Y.shape and residual.dtype == Y.dtype),
-          "residual must have Y's shape and type")
+    if not (x_scale.dtype == w_scale.dtype == torch.float32 and x_scale.numel() == M and
+            w_scale.numel() == N):
+        raise ValueError("x_scale and w_scale must be fp32 [M] and [N]")
+    if Y.shape != (M, N):
+        raise ValueError("Y must be [M][N]")
+    if residual is not None and not (residual.shape == Y.shape and residual.dtype == Y.dtype):
+        raise ValueError("residual must have Y's shape and type")
     kind = _dtype(Y)
     if epilogue is None:
         epilogue = (kind | (BITNET_EPI_SILU if silu else 0) |
                     (BITNET_EPI_RESIDUAL if residual is not None else 0))
-    _need((epilogue & BITNET_EPI_TYPE_MASK) == kind, "epilogue names another type than Y's")
+    elif (epilogue & BITNET_EPI_TYPE_MASK) != kind:
+        raise ValueError("epilogue names another type than Y's")
     _check(library().bitnet_linear_w8(xq, xs, wq, ws, M, N, K, y, epilogue, res,
                                       _stream(stream)))
 
@@ -341,22 +344,21 @@ def bitnet_rope_append(Q, K, V, inv_freq, cu_q, kv_len, block_table, k_cache, v_
         "inv_freq cu_q kv_len block_table k_cache v_cache Q_out q_gain k_gain",
         (inv_freq, cu_q, kv_len, block_table, k_cache, v_cache, Q_out, q_gain, k_gain))
     batch, stride, pages, heads, page, dim = _paged(cu_q, kv_len, block_table, k_cache, v_cache)
-    dtype, device = Q_out.dtype, Q_out.get_device()
-    _need(Q_out.dim() == 2 and Q_out.shape[1] % dim == 0,
-          "Q_out must be [M][q_heads * head_dim]")
-    M, width = Q_out.shape
-    q, ldq = _rows("Q", Q, width, dtype, device)
-    k, ldk = _rows("K", K, heads * dim, dtype, device)
-    v, ldv = _rows("V", V, heads * dim, dtype, device)
-    _need(Q.shape[0] == K.shape[0] == V.shape[0] == M, "Q, K, V and Q_out must have the same rows")
-    _need(inv_freq.dtype == torch.float32, "inv_freq must be fp32")
+    if Q_out.dim() != 2 or Q_out.shape[1] % dim:
+        raise ValueError("Q_out must be [M][q_heads * head_dim]")
+    (M, width), dtype, device = Q_out.shape, Q_out.dtype, Q_out.get_device()
+    ldq = _row_stride("Q", Q, M, width, dtype, device)
+    ldk = _row_stride("K", K, M, heads * dim, dtype, device)
+    ldv = _row_stride("V", V, M, heads * dim, dtype, device)
+    if inv_freq.dtype != torch.float32:
+        raise ValueError("inv_freq must be fp32")
     for g in (q_gain, k_gain):
-        _need(g is None or (g.dtype == torch.float32 and g.numel() == dim),
-              "gains must be fp32 [head_dim]")
+        if g is not None and (g.dtype != torch.float32 or g.numel() != dim):
+            raise ValueError("gains must be fp32 [head_dim]")
     _check(library().bitnet_rope_append(
-        q, ldq, k, ldk, v, ldv, _dtype(Q_out), M, width // dim, heads, dim, inv,
-        2 * inv_freq.numel(), rope | (BITNET_ROPE_HEAD_NORM if head_norm else 0), qg, kg, eps,
-        batch, cu, length, table, stride, kc, vc, pages, page, out, _stream(stream)))
+        Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv, _dtype(Q_out), M, width // dim,
+        heads, dim, inv, 2 * inv_freq.numel(), rope | (BITNET_ROPE_HEAD_NORM if head_norm else 0),
+        qg, kg, eps, batch, cu, length, table, stride, kc, vc, pages, page, out, _stream(stream)))
 
 
 def bitnet_attention_workspace_size(M, batch, q_heads, kv_heads, head_dim):
@@ -379,8 +381,10 @@ def bitnet_attention(Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspac
         "Q cu_q kv_len block_table k_cache v_cache O workspace",
         (Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspace))
     batch, stride, pages, heads, page, dim = _paged(cu_q, kv_len, block_table, k_cache, v_cache)
-    _need(Q.dim() == 2 and Q.shape[1] % dim == 0, "Q must be [M][q_heads * head_dim]")
-    _need(O.shape == Q.shape and O.dtype == Q.dtype, "O must have Q's shape and type")
+    if Q.dim() != 2 or Q.shape[1] % dim:
+        raise ValueError("Q must be [M][q_heads * head_dim]")
+    if O.shape != Q.shape or O.dtype != Q.dtype:
+        raise ValueError("O must have Q's shape and type")
     M, width = Q.shape
     _check(library().bitnet_attention(
         q, _dtype(Q), M, width // dim, heads, dim, dim ** -0.5 if scale is None else scale, batch,

@@ -950,6 +950,25 @@ int launch_attn_dim(const AttnParams& p, int sms, cudaStream_t st) {
   return BITNET_ERR_UNSUPPORTED;                     // attn_shape() keeps these at 16 rows
 }
 
+// Token tile of the int8 product (pure host logic).  A stage of 128 inputs
+// brings 128 weight rows and the tile's tokens into shared memory, which takes
+// longer than its products for every tile up to 256 tokens; the CTAs run
+// ceil(tiles / SMs) waves of tiles.  So the tile is the one with the smallest
+// waves x (128 + tokens), the larger one of equals (fewer reads of the weights).
+int w8_token_tile(int M, int N, int sms) {
+  int best = 256;
+  long long best_cost = -1;
+  for (int bn = 256; bn >= 16; bn /= 2) {
+    const long long tiles = (long long)((M + bn - 1) / bn) * ((N + 127) / 128);
+    const long long cost = (tiles + sms - 1) / sms * (128 + bn);
+    if (best_cost < 0 || cost < best_cost) {
+      best = bn;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 template <class C>
 int launch_w8_cfg(const W8Params& params, const int8_t* Xq, const int8_t* Wq, int K,
                   cudaStream_t st) {
@@ -1507,11 +1526,15 @@ int bitnet_linear_w8(const int8_t* Xq, const float* x_scale, const int8_t* Wq,
   p.out_type = epilogue & BITNET_EPI_TYPE_MASK;
   p.flags = epilogue & ~BITNET_EPI_TYPE_MASK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (M <= 16) return launch_w8_cfg<W8Config<16, 10>>(p, Xq, Wq, K, st);
-  if (M <= 32) return launch_w8_cfg<W8Config<32, 9>>(p, Xq, Wq, K, st);
-  if (M <= 64) return launch_w8_cfg<W8Config<64, 8>>(p, Xq, Wq, K, st);
-  if (M <= 128) return launch_w8_cfg<W8Config<128, 6>>(p, Xq, Wq, K, st);
-  return launch_w8_cfg<W8Config<256, 4>>(p, Xq, Wq, K, st);
+  DeviceInfo di;
+  if (int rc = device_info(di)) return rc;
+  switch (w8_token_tile(M, N, di.sms)) {
+    case 16: return launch_w8_cfg<W8Config<16, 10>>(p, Xq, Wq, K, st);
+    case 32: return launch_w8_cfg<W8Config<32, 9>>(p, Xq, Wq, K, st);
+    case 64: return launch_w8_cfg<W8Config<64, 8>>(p, Xq, Wq, K, st);
+    case 128: return launch_w8_cfg<W8Config<128, 6>>(p, Xq, Wq, K, st);
+    default: return launch_w8_cfg<W8Config<256, 4>>(p, Xq, Wq, K, st);
+  }
 }
 
 int bitnet_rope_append(const void* Q, int64_t q_stride, const void* K, int64_t k_stride,

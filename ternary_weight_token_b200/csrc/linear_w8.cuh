@@ -49,7 +49,10 @@ struct W8Config {
   static constexpr int BK = 128;
   static constexpr int STAGES = STAGES_;
   static constexpr int W_STAGE = BM * BK, X_STAGE = BN * BK;
-  static constexpr int THREADS = 256;
+  // two groups of four epilogue warps share a tile's tokens where they have
+  // 64 or more: one group alone is slower than the products it follows
+  static constexpr int GROUPS = BN >= 64 ? 2 : 1;
+  static constexpr int THREADS = 128 + 128 * GROUPS;
   static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
   static constexpr int OFF_X = STAGES * W_STAGE;
   static constexpr int OFF_BAR = OFF_X + STAGES * X_STAGE;
@@ -92,18 +95,20 @@ __device__ __forceinline__ void w8_store(const uint32_t (&v)[CW], float wf, cons
       for (int j = 0; j < CW; ++j, q += stride) r[j] = j < live ? static_cast<float>(*q) : 0.0f;
     }
     T* y = reinterpret_cast<T*>(Y) + at;
-#pragma unroll
-    for (int j = 0; j < CW; ++j, y += stride) {
-      // the sum, two reciprocals, their product and the last product: 2^-24 each
+    // the sum, two reciprocals, their product and the last product: 2^-24 each
+    auto value = [&](int j) {
       float x = __fmul_rn(__int2float_rn((int)v[j]), __fmul_rn(wf, tok[j]));
       if constexpr (SILU) x = silu_f32(x);
       if constexpr (RESID) x = __fadd_rn(r[j], x);
-      if (j < live) {
-        if constexpr (TYPE == OUT_BF16)
-          *y = __float2bfloat16_rn(x);
-        else
-          *y = x;
-      }
+      return static_cast<T>(x);
+    };
+    if (live == CW) {                            // a full step: no test per token
+#pragma unroll
+      for (int j = 0; j < CW; ++j, y += stride) *y = value(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < CW; ++j, y += stride)
+        if (j < live) *y = value(j);
     }
   }
 }
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
-      mbar_init(&accempty[b], 4);
+      mbar_init(&accempty[b], 4 * C::GROUPS);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_wait(drain, 0, nullptr, 100000000ull);
     }
   } else if (warp >= 4) {
-    const int q = warp & 3, et = threadIdx.x - 128;
+    const int q = warp & 3, group = (warp - 4) >> 2, et = threadIdx.x - 128;
     const uint32_t lane_base = tbase + ((uint32_t)(32 * q) << 16);
     uint32_t tcount = 0;
     for (int tile = blockIdx.x; tile < p.num_tiles; tile += gridDim.x, ++tcount) {
@@ -211,21 +216,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int n = tn * C::BM + 32 * q + lane;
       const bool n_ok = n < p.N;
       float* tok = s_tok + ab * C::BN;           // read last two tiles ago
-      for (int j = et; j < C::BN; j += 128)
+      for (int j = et; j < C::BN; j += 128 * C::GROUPS)
         tok[j] = m0 + j < p.M ? __fdiv_rn(1.0f, p.xs[m0 + j]) : 0.0f;
       const float wf = n_ok ? __fdiv_rn(1.0f, p.ws[n]) : 0.0f;
-      named_bar_sync(1, 128);
+      named_bar_sync(1, 128 * C::GROUPS);
       if (!mbar_wait(&accfull[ab], aph, abort_flag)) break;
       tc_fence_after();
-      constexpr int CW = C::BN < 32 ? C::BN : 32;    // columns per step
+      constexpr int CW = 16;                      // tokens per step
 #pragma unroll 1
-      for (int c = 0; c < C::BN; c += CW) {
+      for (int c = CW * group; c < C::BN; c += CW * C::GROUPS) {
         if (m0 + c >= p.M) break;
         uint32_t v[CW];
-        if constexpr (CW == 32)
-          tmem_ld_32x32b_x32(lane_base + ab * C::BN + c, v);
-        else
-          tmem_ld_32x32b_x16(lane_base + ab * C::BN + c, v);
+        tmem_ld_32x32b_x16(lane_base + ab * C::BN + c, v);
         tmem_ld_wait();
         if (n_ok) {
           const size_t at = (size_t)(m0 + c) * p.N + n;
