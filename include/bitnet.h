@@ -330,8 +330,8 @@ BITNET_API size_t bitnet_attention_workspace_size(int M, int batch, int q_heads,
  * The token at position p attends to positions 0 .. p of its sequence; one
  * with none (a negative position) gives zeros.  Scores, softmax statistics and
  * sums are fp32; BF16 calls round the probabilities to bf16 before their
- * product with V, F32 calls carry them in 16 bits and Q in 24.  Slots past a
- * sequence's length may hold anything, NaN included.  The workspace needs no
+ * product with V, F32 calls carry Q and the probabilities in 24 bits.  Slots
+ * past a sequence's length may hold anything, NaN included.  The workspace needs no
  * initialisation; calls that share one must not overlap on the GPU.  O must
  * not overlap Q.  Errors: INVALID_ARG, WORKSPACE, CUDA. */
 BITNET_API int bitnet_attention(const void *Q, int dtype, int M, int q_heads, int kv_heads,

@@ -273,9 +273,10 @@ __device__ __forceinline__ float ex2(float x) {
 // every block with its own statistics, joined in shared memory at the end.
 // WR = 4 takes 64 rows of a chunk.
 //
-// fp32 queries (F32): q is held as three bf16 terms (24 bits, exact) and the
-// probabilities as two (16 bits, 2^-17 relative), so products with the bf16
-// cache carry fp32-like accuracy for 3 + 2 instead of 1 + 1 matrix products.
+// fp32 queries (F32): q and the probabilities are held as three bf16 terms (24
+// bits, exact), so their products with the bf16 cache are those of fp32, for
+// three matrix products in place of one.  (Two terms of the probabilities left
+// a relative error of 1.6e-6, three 2e-7.)
 // bf16 queries round the probabilities to bf16 (2^-9 relative, averaged over
 // the keys, below the rounding of the output); l sums the unrounded ones.
 template <int DP, int WR, bool F32>
@@ -508,6 +509,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
           o[n][3] *= alpha[1];
         }
       }
+      uint32_t pf[C::KW / 16][C::TERMS][4];          // the probabilities' terms
 #pragma unroll
       for (int n = 0; n < C::KW / 16; ++n) {
         float e[8];
@@ -516,28 +518,43 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
           e[k] = ex2(z[2 * n + (k >> 2)][k & 3] - base[(k >> 1) & 1]);
           l[(k >> 1) & 1] += e[k];
         }
-        uint32_t ph[4], pl[4];
-        ph[0] = pack_bf16x2(e[0], e[1]);
-        ph[1] = pack_bf16x2(e[2], e[3]);
-        ph[2] = pack_bf16x2(e[4], e[5]);
-        ph[3] = pack_bf16x2(e[6], e[7]);
-        if constexpr (F32) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            pl[k] = pack_bf16x2(e[2 * k] - __uint_as_float(ph[k] << 16),
-                                e[2 * k + 1] - __uint_as_float(ph[k] & 0xffff0000u));
+        for (int t = 0; t < C::TERMS; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            pf[n][t][k] = pack_bf16x2(e[2 * k], e[2 * k + 1]);
+            if constexpr (F32) {
+              e[2 * k] -= __uint_as_float(pf[n][t][k] << 16);
+              e[2 * k + 1] -= __uint_as_float(pf[n][t][k] & 0xffff0000u);
+            }
+          }
+      }
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) {
+        // fp32: a block's sum starts at zero and is added rounded, since a
+        // matrix instruction truncates its running sum (over thousands of
+        // keys that came to 1.6e-6)
+        float t0[4], t1[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          t0[k] = F32 ? 0.0f : o[2 * d][k];
+          t1[k] = F32 ? 0.0f : o[2 * d + 1][k];
         }
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) {
+        for (int n = 0; n < C::KW / 16; ++n) {
           uint32_t v0, v1, v2, v3;
           ldmatrix_x4_trans(attn_at<C::ROW>(sv, C::KW * wk + 16 * n + (lane & 15),
                                             2 * d + (lane >> 4)), v0, v1, v2, v3);
-          if constexpr (F32) {
-            mma_bf16(o[2 * d], pl, v0, v1);
-            mma_bf16(o[2 * d + 1], pl, v2, v3);
+#pragma unroll
+          for (int t = C::TERMS - 1; t >= 0; --t) {
+            mma_bf16(t0, pf[n][t], v0, v1);
+            mma_bf16(t1, pf[n][t], v2, v3);
           }
-          mma_bf16(o[2 * d], ph, v0, v1);
-          mma_bf16(o[2 * d + 1], ph, v2, v3);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          o[2 * d][k] = F32 ? o[2 * d][k] + t0[k] : t0[k];
+          o[2 * d + 1][k] = F32 ? o[2 * d + 1][k] + t1[k] : t1[k];
         }
       }
     }

@@ -1588,14 +1588,19 @@ int bitnet_rope_append(const void* Q, int64_t q_stride, const void* K, int64_t k
   p.inv_freq = inv_freq; p.qg = q_gain; p.kg = k_gain; p.eps = eps;
   p.qh = q_heads; p.kvh = kv_heads; p.D = head_dim; p.rot = rot_dim;
   p.interleaved = (flags & BITNET_ROPE_INTERLEAVED) ? 1 : 0;
-  p.tokens = M >= di.sms * 16 ? 4 : 1;
+  // a warp per token once that fills the GPU, up to a CTA per token below
+  const int warps = kRopeThreads / 32;
+  p.warps_per_token = warps;
+  while (p.warps_per_token > 1 && (long long)M * p.warps_per_token > di.sms * 32ll)
+    p.warps_per_token /= 2;
   const bool bf = dtype == BITNET_BF16;
   void (*kern)(RopeParams) =
       bf ? (norm ? rope_append_kernel<true, true> : rope_append_kernel<true, false>)
          : (norm ? rope_append_kernel<false, true> : rope_append_kernel<false, false>);
-  const size_t smem = (size_t)p.tokens * (head_dim / 2) * sizeof(float2);
-  return launch_pdl(kern, dim3((unsigned)((M + p.tokens - 1) / p.tokens)), dim3(kRopeThreads),
-                    smem, reinterpret_cast<cudaStream_t>(stream), p);
+  const size_t smem = (size_t)warps * (head_dim / 2) * sizeof(float2);
+  const long long ctas = ((long long)M * p.warps_per_token + warps - 1) / warps;
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kRopeThreads), smem,
+                    reinterpret_cast<cudaStream_t>(stream), p);
 }
 
 size_t bitnet_attention_workspace_size(int M, int batch, int q_heads, int kv_heads,

@@ -14,9 +14,11 @@
 //
 // Bound by memory: a token of the 2B model reads 7.5 KB and writes 7.5 KB.  A
 // group of lanes owns one head and moves it in 16-byte loads and stores (eight
-// bf16 or four fp32 pairs per lane); the head's values are loaded before the
-// CTA looks its tokens up and forms their cosines and sines, which all heads
-// of the token then share.
+// bf16 or four fp32 pairs per lane).  A warp serves one token, or a part of
+// its heads where tokens are few: it looks the token up and forms its cosines
+// and sines by itself, so warps never wait for one another, and a lane keeps
+// the few angles of its place in the head in registers for all heads.  The
+// first heads are loaded before the token is looked up.
 #pragma once
 
 #include "common.cuh"
@@ -36,6 +38,7 @@ struct PagedBatch {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 256;
+constexpr int kRopeDepth = 1;          // heads a lane group has in flight
 
 struct RopeParams {
   PagedBatch pb;
@@ -48,7 +51,7 @@ struct RopeParams {
   float eps;
   int qh, kvh, D, rot;
   int interleaved;
-  int tokens;                       // per CTA, at most one per warp
+  int warps_per_token;              // a power of two up to the CTA's warps
 };
 
 // Sequence of token row r: the number of sequences that end at or before it
@@ -142,98 +145,93 @@ __device__ __forceinline__ void rope_runs(int j, int n, const RopeParams& p, int
 
 template <bool BF16, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p) {
-  extern __shared__ float2 s_cs[];               // [tokens][D / 2] cosine, sine
-  __shared__ int s_pos[kRopeThreads / 32];       // position, or -1: leave the row out
-  __shared__ long long s_dst[kRopeThreads / 32]; // first element of the row's head 0, or -1
-  constexpr int N = RopeVec<BF16>::N;
+  extern __shared__ float2 s_cs[];               // [warps][D / 2] cosine, sine
+  constexpr int N = RopeVec<BF16>::N, ESZ = BF16 ? 2 : 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int D = p.D, half_d = D / 2;
   const int lanes = half_d / N;                  // lane slots of a head
   int width = 1;                                 // lanes of a group: a power of two
   while (width < lanes) width *= 2;
-  const int j = threadIdx.x & (width - 1);
-  const int group = threadIdx.x / width, groups = kRopeThreads / width;
+  const int j = lane & (width - 1);
+  const bool active = j < lanes;
+  const int slots = 32 / width;                  // heads of a warp at a time
   const int heads = p.qh + 2 * p.kvh;
-  const int r0 = blockIdx.x * p.tokens;
+  const int gw = blockIdx.x * (kRopeThreads / 32) + warp;
+  const int r = gw / p.warps_per_token, part = gw - r * p.warps_per_token;
+  const int h0 = part * slots + lane / width, step = slots * p.warps_per_token;
   int e0, e1;
-  rope_runs(j < lanes ? j : 0, N, p, e0, e1);
+  rope_runs(active ? j : 0, N, p, e0, e1);
 
   grid_launch_dependents();
   grid_dependency_wait();
+  if (r >= p.pb.M) return;
 
-  // the group's first head goes in flight before the tokens are looked up
-  auto load = [&](int unit, uint4& a, uint4& b) {
-    const int t = unit / heads, h = unit - t * heads;
-    const int r = r0 + t;
-    if (t >= p.tokens || r >= p.pb.M || j >= lanes) return;
-    const bool isq = h < p.qh, isk = h < p.qh + p.kvh;
-    const void* src = isq ? p.Q : isk ? p.K : p.V;
-    const long long off = isq   ? (long long)r * p.ldq + (long long)h * D
-                          : isk ? (long long)r * p.ldk + (long long)(h - p.qh) * D
-                                : (long long)r * p.ldv + (long long)(h - p.qh - p.kvh) * D;
-    const char* base = reinterpret_cast<const char*>(src) + off * (BF16 ? 2 : 4);
-    a = *reinterpret_cast<const uint4*>(base + e0 * (BF16 ? 2 : 4));
-    b = *reinterpret_cast<const uint4*>(base + e1 * (BF16 ? 2 : 4));
+  const char* qrow = reinterpret_cast<const char*>(p.Q) + (long long)r * p.ldq * ESZ;
+  const char* krow = reinterpret_cast<const char*>(p.K) + (long long)r * p.ldk * ESZ;
+  const char* vrow = reinterpret_cast<const char*>(p.V) + (long long)r * p.ldv * ESZ;
+  auto load = [&](int h, uint4& x, uint4& y) {
+    x = y = make_uint4(0, 0, 0, 0);
+    if (h >= heads || !active) return;
+    const char* base = h < p.qh           ? qrow + h * D * ESZ
+                       : h < p.qh + p.kvh ? krow + (h - p.qh) * D * ESZ
+                                          : vrow + (h - p.qh - p.kvh) * D * ESZ;
+    x = *reinterpret_cast<const uint4*>(base + e0 * ESZ);
+    y = *reinterpret_cast<const uint4*>(base + e1 * ESZ);
   };
-  uint4 a = make_uint4(0, 0, 0, 0), b = a;
-  load(group, a, b);
+  uint4 a[kRopeDepth], b[kRopeDepth];
+#pragma unroll
+  for (int k = 0; k < kRopeDepth; ++k) load(h0 + k * step, a[k], b[k]);
 
-  if (warp < p.tokens) {                         // one warp looks one token up
-    const int r = r0 + warp;
-    int pos = -1;
-    long long dst = -1;
-    if (r < p.pb.M) {
-      const int s = sequence_of(p.pb, r, lane);
-      if (s < p.pb.batch) {
-        const int c0 = __ldg(p.pb.cu_q + s), c1 = __ldg(p.pb.cu_q + s + 1);
-        const int len = __ldg(p.pb.kv_len + s);
-        pos = len - (c1 - r);
-        // c0 > r only in a table of rows that does not rise
-        if (pos < 0 || r < c0) {
-          pos = -1;
-        } else if (pos / p.pb.page_size >= p.pb.stride) {
-          if (lane == 0) record_device_error(DEV_ERR_INDEX);
-        } else {
-          const int page = __ldg(p.pb.table + (long long)s * p.pb.stride + pos / p.pb.page_size);
-          if (page < 0 || page >= p.pb.num_pages) {
-            if (lane == 0) record_device_error(DEV_ERR_INDEX);
-          } else {
-            dst = ((long long)page * p.kvh * p.pb.page_size + pos % p.pb.page_size) * D;
-          }
-        }
-      }
-    }
-    if (lane == 0) {
-      s_pos[warp] = pos;
-      s_dst[warp] = dst;
+  // ---- the token's place
+  int pos;
+  long long dst = -1;                            // first element of its head 0 in the cache
+  {
+    const int s = sequence_of(p.pb, r, lane);
+    if (s >= p.pb.batch) return;                 // behind the last sequence
+    const int c0 = __ldg(p.pb.cu_q + s), c1 = __ldg(p.pb.cu_q + s + 1);
+    pos = __ldg(p.pb.kv_len + s) - (c1 - r);
+    // c0 > r only in a table of rows that does not rise
+    if (pos < 0 || r < c0) return;
+    const int at = pos / p.pb.page_size;
+    int page = -1;
+    if (at < p.pb.stride) page = __ldg(p.pb.table + (long long)s * p.pb.stride + at);
+    if (page < 0 || page >= p.pb.num_pages) {
+      if (lane == 0) record_device_error(DEV_ERR_INDEX);
+    } else {
+      dst = ((long long)page * p.kvh * p.pb.page_size + (pos - at * p.pb.page_size)) * D;
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.tokens * half_d; i += kRopeThreads) {
-    const int t = i / half_d, f = i - t * half_d;
+  float2* cs_row = s_cs + warp * half_d;
+  for (int f = lane; f < half_d; f += 32) {
     float2 cs = make_float2(1.0f, 0.0f);
-    if (f < p.rot / 2 && s_pos[t] >= 0) {
+    if (f < p.rot / 2) {
       // turns = p * inv_freq / (2 pi); the nearest whole turn is dropped in fp64
-      double turns = (double)s_pos[t] * (double)__ldg(p.inv_freq + f) * 0.15915494309189533577;
+      double turns = (double)pos * (double)__ldg(p.inv_freq + f) * 0.15915494309189533577;
       turns -= rint(turns);
       sincospif((float)(2.0 * turns), &cs.y, &cs.x);
     }
-    s_cs[i] = cs;
+    cs_row[f] = cs;
   }
-  __syncthreads();
+  __syncwarp();
+  float2 cs[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) cs[i] = cs_row[N * (active ? j : 0) + i];
 
   // every lane of a warp makes the same number of trips: the norm's sums go
   // through warp shuffles
-  const int units = p.tokens * heads, warp_group0 = (threadIdx.x & ~31) / width;
-  for (int unit = group, first = warp_group0; first < units; unit += groups, first += groups) {
-    uint4 na = make_uint4(0, 0, 0, 0), nb = na;
-    load(unit + groups, na, nb);
-    const int t = unit < units ? unit / heads : 0, h = unit - t * heads;
+  for (int h = h0, first = part * slots; first < heads; h += step, first += step) {
+    const uint4 ua = a[0], ub = b[0];
+#pragma unroll
+    for (int k = 0; k + 1 < kRopeDepth; ++k) {
+      a[k] = a[k + 1];
+      b[k] = b[k + 1];
+    }
+    load(h + kRopeDepth * step, a[kRopeDepth - 1], b[kRopeDepth - 1]);
     const bool isq = h < p.qh, isv = h >= p.qh + p.kvh;
-    const bool live = unit < units && j < lanes && s_pos[t] >= 0;
+    const bool live = h < heads && active;
     float x[2 * N];
-    RopeVec<BF16>::unpack(a, x);
-    RopeVec<BF16>::unpack(b, x + N);
+    RopeVec<BF16>::unpack(ua, x);
+    RopeVec<BF16>::unpack(ub, x + N);
     float rr = 1.0f;
     if (NORM) {
       float sum = 0.0f;                          // idle lanes hold zeros
@@ -251,30 +249,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p)
           x[N + i] = x[N + i] * rr * (g ? __ldg(g + e1 + i) : 1.0f);
         }
       }
-      // pair index of the run's first pair
-      const float2* cs = s_cs + t * half_d + N * (j < lanes ? j : 0);
-      float y[2 * N];
+      if (p.interleaved) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float2 w = cs[i];
-        const float u = p.interleaved ? x[2 * i] : x[i];
-        const float v = p.interleaved ? x[2 * i + 1] : x[N + i];
-        const float c = __fmaf_rn(u, w.x, -__fmul_rn(v, w.y));
-        const float d = __fmaf_rn(v, w.x, __fmul_rn(u, w.y));
-        if (p.interleaved) {
-          y[2 * i] = c;
-          y[2 * i + 1] = d;
-        } else {
-          y[i] = c;
-          y[N + i] = d;
+        for (int i = 0; i < N; ++i) {
+          const float u = x[2 * i], v = x[2 * i + 1];
+          x[2 * i] = __fmaf_rn(u, cs[i].x, -__fmul_rn(v, cs[i].y));
+          x[2 * i + 1] = __fmaf_rn(v, cs[i].x, __fmul_rn(u, cs[i].y));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float u = x[i], v = x[N + i];
+          x[i] = __fmaf_rn(u, cs[i].x, -__fmul_rn(v, cs[i].y));
+          x[N + i] = __fmaf_rn(v, cs[i].x, __fmul_rn(u, cs[i].y));
         }
       }
-#pragma unroll
-      for (int i = 0; i < 2 * N; ++i) x[i] = y[i];
     }
     if (live) {
       if (isq) {
-        const long long o = (long long)(r0 + t) * p.qh * D + (long long)h * D;
+        const long long o = ((long long)r * p.qh + h) * D;
         if (BF16) {
           __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.Qo) + o;
           store_bf16<N>(out + e0, x);
@@ -284,16 +277,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p)
           store_f32<N>(out + e0, x);
           store_f32<N>(out + e1, x + N);
         }
-      } else if (s_dst[t] >= 0) {
+      } else if (dst >= 0) {
         const int kh = isv ? h - p.qh - p.kvh : h - p.qh;
-        __nv_bfloat16* out =
-            (isv ? p.Vc : p.Kc) + s_dst[t] + (long long)kh * p.pb.page_size * D;
+        __nv_bfloat16* out = (isv ? p.Vc : p.Kc) + dst + (long long)kh * p.pb.page_size * D;
         store_bf16<N>(out + e0, x);
         store_bf16<N>(out + e1, x + N);
       }
     }
-    a = na;
-    b = nb;
   }
 }
 

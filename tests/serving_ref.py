@@ -70,12 +70,12 @@ def attention_tolerance(dtype, o, a, smax, D):
     """Bounds of the roundings.  Scores: a matrix instruction adds 16 products with one
     truncation (2^-23 of the partial sums, at most smax), D / 16 times per term (one term of q for
     bf16, three for fp32); the error enters numerator and denominator.  exp2 adds 2^-21 with its
-    argument's rounding.  Probabilities: bf16 2^-8, two-term fp32 2^-16.  The output's rounding:
+    argument's rounding.  Probabilities: bf16 2^-8, fp32 (three terms) 2^-24.  The output's rounding:
     2^-8 or 2^-24 of its value."""
     terms = 3 if dtype == F32 else 1
     score = 2 * 1.4427 * terms * (D / 16) * 2.0 ** -23 * smax + 2.0 ** -20
     if dtype == F32:
-        return a * (2.0 ** -16 + score) + o.abs() * 2.0 ** -24 + 1e-30
+        return a * (2.0 ** -24 + score) + o.abs() * 2.0 ** -24 + 1e-30
     return a * (2.0 ** -8 + score) + o.abs() * 2.0 ** -8 + 1e-30
 
 
