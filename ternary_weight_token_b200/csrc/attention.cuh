@@ -33,7 +33,7 @@ namespace bitnet {
 
 constexpr int kAttnThreads = 128;
 constexpr int kAttnTile = 64;          // keys per block of the mma.sync kernel
-constexpr int kAttnPlanHead = 2;       // words of the plan before the sequences'
+constexpr int kAttnPlanHead = 3;       // words of the plan before the sequences'
 constexpr int kAttnTarget = 592;       // most shares of a call (mma.sync kernel)
 
 struct AttnParams {
@@ -46,7 +46,7 @@ struct AttnParams {
   int rt_shift, unit_shift;            // log2 of the rows per tile and the keys per block
   int min_units;                       // smallest share
   int target;                          // shares wanted, 0: whole items, dealt out in turn
-  long long* plan;                     // units per share, alignment; units before each sequence
+  long long* plan;                     // units per share, alignment, units; then units before each sequence
   float* part;                         // slots: m[RT], l[RT], o[RT][D]
 };
 
@@ -135,6 +135,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
     if (tid == 0) {
       p.plan[0] = share;
       p.plan[1] = align;
+      p.plan[2] = total;
     }
     long long at = sum - mine;
     for (int b = b0; b < b1; ++b) {
@@ -655,85 +656,116 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
 }
 
 // --------------------------------------------------------------- the join
-// One CTA per token row and query head.  The shares that hold parts of its
-// item follow from the item's place on the line of units and the share that
-// the attention kernel left in the plan: the first one wrote slot 2 s + 1, the
-// others slot 2 s.  Warps take the parts in turn, lanes the D values.
-template <bool F32>
+// CTA (c, y) joins the item that starts in share c and goes on past its end, if
+// there is one: rows y, y + gridDim.y, ... of it (WIDE: four warps take a row
+// each; else they take one row's parts in turn).  The first part is in slot
+// 2 c + 1, those of the shares after it in slots 2 (c + 1), 2 (c + 2), ...
+// Lanes hold 8 values each.
+template <bool F32, bool WIDE>
 __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
   __shared__ float s_o[4][kRopeMaxDim];
   __shared__ float s_ml[4][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int r = blockIdx.x, qhead = blockIdx.y;
-  const long long share = p.plan[0];
+  const long long share = p.plan[0], total = p.plan[2];
   const int align = (int)p.plan[1];
-  const int b = sequence_of(p.pb, r, lane);
-  if (b >= p.pb.batch) return;
-  const long long before = p.plan[kAttnPlanHead + b];
-  const SeqWork w = seq_work(p, b, false, align);
-  if (w.n == 0 || r < w.c0) return;
-  const int RT = 1 << p.rt_shift;
-  const int head = qhead / p.G;
-  const int row = (r - w.c0) * p.G + qhead % p.G;
-  const int rt = row & (RT - 1);
-  const long long item =
-      before + ((long long)(w.tiles - 1 - (row >> p.rt_shift)) * p.kvh + head) * w.units;
-  const int first = (int)(item / share);
-  const int splits = (int)((item + w.units - 1) / share) - first + 1;
-  if (splits == 1) return;
-  const long long size = (long long)RT * (p.D + 2);
-  auto part = [&](int s) { return p.part + (2ll * (first + s) + (s == 0 ? 1 : 0)) * size; };
-  const int per = p.D / 8;                           // 8 values per lane, up to 32 lanes
-  // one pass with a running maximum: a part's statistics and sums are loaded
-  // together, four parts in flight
-  float m = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-  for (int s = warp; s < splits; s += 4) {
-    const float* q = part(s);
-    const float ms = q[rt], ls = q[RT + rt];
-    float4 x = make_float4(0, 0, 0, 0), y = x;
-    if (lane < per) {
-      const float4* v = reinterpret_cast<const float4*>(q + 2 * RT + rt * p.D + 8 * lane);
-      x = v[0];
-      y = v[1];
+  const int c = blockIdx.x;
+  const long long end = share * (c + 1);
+  if (end >= total) return;
+  // the sequence that holds unit end - 1: the last one that starts before it
+  int b = -1;
+  for (int base = 0; base < p.pb.batch; base += 128) {
+    int in = 0;
+    bool starts[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = base + 32 * k + lane;
+      starts[k] = i < p.pb.batch && p.plan[kAttnPlanHead + i] < end;
     }
-    const float mm = fmaxf(m, ms), base = mm == -INFINITY ? 0.0f : mm;
-    const float f = ex2(m - base), g = ex2(ms - base);
-    m = mm;
-    l = l * f + ls * g;
-    o[0] = o[0] * f + x.x * g; o[1] = o[1] * f + x.y * g;
-    o[2] = o[2] * f + x.z * g; o[3] = o[3] * f + x.w * g;
-    o[4] = o[4] * f + y.x * g; o[5] = o[5] * f + y.y * g;
-    o[6] = o[6] * f + y.z * g; o[7] = o[7] * f + y.w * g;
-  }
-  if (lane == 0) {
-    s_ml[warp][0] = m;
-    s_ml[warp][1] = l;
-  }
-  if (lane < per) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s_o[warp][8 * lane + k] = o[k];
+    for (int k = 0; k < 4; ++k) in += __popc(__ballot_sync(0xffffffffu, starts[k]));
+    b += in;
+    if (in < 128) break;
   }
-  __syncthreads();
-  float mm = -INFINITY, sum = 0.0f, f[4];
+  const SeqWork w = seq_work(p, b, false, align);
+  const long long at = p.plan[kAttnPlanHead + b];
+  const int local = (int)((end - 1 - at) / w.units);
+  const long long item = at + (long long)local * w.units;
+  if (item + w.units <= end || item < end - share) return;   // does not go on, or began before
+  const int splits = (int)((item + w.units - 1) / share) - c + 1;
+  const AttnPiece q = piece_of(p, b, w, local, 0, w.units, -1);
+
+  const int RT = 1 << p.rt_shift, per = p.D / 8;
+  const long long size = (long long)RT * (p.D + 2);
+  const float* part0 = p.part + (2ll * c + 1) * size;
+  const float* part1 = p.part + (2ll * c + 2) * size;        // further parts: 2 size apart
+  for (int rt = WIDE ? blockIdx.y * 4 + warp : blockIdx.y; rt < q.nrows;
+       rt += WIDE ? gridDim.y * 4 : gridDim.y) {
+    // one pass with a running maximum: a part's statistics and sums are loaded
+    // together, several parts in flight
+    float m = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = WIDE ? 0 : warp; s < splits; s += WIDE ? 1 : 4) {
+      const float* f = s == 0 ? part0 : part1 + 2 * (s - 1) * size;
+      const float ms = f[rt], ls = f[RT + rt];
+      float4 x = make_float4(0, 0, 0, 0), y = x;
+      if (lane < per) {
+        const float4* v = reinterpret_cast<const float4*>(f + 2 * RT + rt * p.D + 8 * lane);
+        x = v[0];
+        y = v[1];
+      }
+      const float mm = fmaxf(m, ms), base = mm == -INFINITY ? 0.0f : mm;
+      const float e = ex2(m - base), g = ex2(ms - base);
+      m = mm;
+      l = l * e + ls * g;
+      o[0] = o[0] * e + x.x * g; o[1] = o[1] * e + x.y * g;
+      o[2] = o[2] * e + x.z * g; o[3] = o[3] * e + x.w * g;
+      o[4] = o[4] * e + y.x * g; o[5] = o[5] * e + y.y * g;
+      o[6] = o[6] * e + y.z * g; o[7] = o[7] * e + y.w * g;
+    }
+    const int rr = q.row0 + rt;
+    const long long off =
+        ((long long)(q.c0 + rr / p.G) * p.qh + (long long)q.head * p.G + rr % p.G) * p.D;
+    if constexpr (WIDE) {
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) mm = fmaxf(mm, s_ml[k][0]);
+      for (int k = 0; k < 8; ++k) o[k] *= inv;
+      if (lane < per) {
+        if constexpr (F32)
+          store_f32<8>(reinterpret_cast<float*>(p.O) + off + 8 * lane, o);
+        else
+          store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(p.O) + off + 8 * lane, o);
+      }
+    } else {
+      if (lane == 0) {
+        s_ml[warp][0] = m;
+        s_ml[warp][1] = l;
+      }
+      if (lane < per) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[k] = mm == -INFINITY ? 0.0f : ex2(s_ml[k][0] - mm);
-    sum += f[k] * s_ml[k][1];
-  }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  for (int d = tid; d < p.D; d += kAttnThreads) {
-    const float x = inv * (f[0] * s_o[0][d] + f[1] * s_o[1][d] + f[2] * s_o[2][d] +
-                           f[3] * s_o[3][d]);
-    const long long off = ((long long)r * p.qh + qhead) * p.D + d;
-    if (F32)
-      reinterpret_cast<float*>(p.O)[off] = x;
-    else
-      reinterpret_cast<__nv_bfloat16*>(p.O)[off] = __float2bfloat16_rn(x);
+        for (int k = 0; k < 8; ++k) s_o[warp][8 * lane + k] = o[k];
+      }
+      __syncthreads();
+      float mm = -INFINITY, sum = 0.0f, f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mm = fmaxf(mm, s_ml[k][0]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[k] = mm == -INFINITY ? 0.0f : ex2(s_ml[k][0] - mm);
+        sum += f[k] * s_ml[k][1];
+      }
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      for (int d = tid; d < p.D; d += kAttnThreads) {
+        const float x = inv * (f[0] * s_o[0][d] + f[1] * s_o[1][d] + f[2] * s_o[2][d] +
+                               f[3] * s_o[3][d]);
+        if (F32)
+          reinterpret_cast<float*>(p.O)[off + d] = x;
+        else
+          reinterpret_cast<__nv_bfloat16*>(p.O)[off + d] = __float2bfloat16_rn(x);
+      }
+      __syncthreads();
+    }
   }
 }
 

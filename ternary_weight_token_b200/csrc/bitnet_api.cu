@@ -901,7 +901,7 @@ AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, 
 }
 
 template <int DP>
-int launch_attn_tc(const AttnParams& p, int sms, cudaStream_t st) {
+int launch_attn_tc(AttnParams& p, int sms, cudaStream_t st) {
   using C = AttnTcConfig<DP>;
   // page pieces that neither a page nor a block of keys cuts
   int box = 16;
@@ -920,30 +920,29 @@ int launch_attn_tc(const AttnParams& p, int sms, cudaStream_t st) {
     return rc;
   auto kern = attn_tc_kernel<DP>;
   if (int rc = set_smem_attr((const void*)kern, C::SMEM)) return rc;
-  AttnParams q = p;
-  if (q.target > sms) q.target = sms;
+  if (p.target > sms) p.target = sms;
   const long long items = ((long long)p.pb.M * p.G / C::RT + p.pb.batch) * p.kvh;
-  const int grid = q.target > 0 ? q.target : (int)std::min<long long>(items, sms);
-  return launch_pdl(kern, dim3(grid), dim3(kAttnTcThreads), C::SMEM, st, mk, mv, q, box);
+  const int grid = p.target > 0 ? p.target : (int)std::min<long long>(items, sms);
+  return launch_pdl(kern, dim3(grid), dim3(kAttnTcThreads), C::SMEM, st, mk, mv, p, box);
 }
 
 template <int DP, int WR, bool F32>
-int launch_attn_rows(const AttnParams& p, int sms, cudaStream_t st) {
+int launch_attn_rows(AttnParams& p, int sms, cudaStream_t st) {
   using C = AttnConfig<DP, WR, F32>;
   void (*kern)(AttnParams) = attn_rows_kernel<DP, WR, F32>;
   if (int rc = set_smem_attr((const void*)kern, C::SMEM)) return rc;
   int per_sm = 0;
   if (int rc = occupancy(per_sm, (const void*)kern, kAttnThreads, C::SMEM)) return rc;
-  AttnParams q = p;
+  // shares: a CTA each, all resident
   const int cap = sms * (per_sm < 1 ? 1 : per_sm);
-  if (q.target > cap) q.target = cap;
+  if (p.target > cap) p.target = cap;
   const long long items = ((long long)p.pb.M * p.G / C::RT + p.pb.batch) * p.kvh;   // at most
-  const int grid = q.target > 0 ? q.target : (int)std::min<long long>(items, cap);
-  return launch_pdl(kern, dim3(grid), dim3(kAttnThreads), C::SMEM, st, q);
+  const int grid = p.target > 0 ? p.target : (int)std::min<long long>(items, cap);
+  return launch_pdl(kern, dim3(grid), dim3(kAttnThreads), C::SMEM, st, p);
 }
 
 template <int WR, bool F32>
-int launch_attn_dim(const AttnParams& p, int sms, cudaStream_t st) {
+int launch_attn_dim(AttnParams& p, int sms, cudaStream_t st) {
   if (p.D <= 64) return launch_attn_rows<64, WR, F32>(p, sms, st);
   if (p.D <= 128) return launch_attn_rows<128, WR, F32>(p, sms, st);
   if constexpr (WR == 1) return launch_attn_rows<256, WR, F32>(p, sms, st);
@@ -1668,8 +1667,17 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   else
     rc = f32 ? launch_attn_dim<4, true>(p, di.sms, st) : launch_attn_dim<4, false>(p, di.sms, st);
   if (rc || p.target == 0) return rc;
-  return launch_pdl(f32 ? attn_join_kernel<true> : attn_join_kernel<false>,
-                    dim3((unsigned)M, (unsigned)q_heads), dim3(kAttnThreads), 0, st, p);
+  // a CTA per share, and per row of its item (16 rows at most, or that many
+  // per sequence on average), or per 32 rows of a wide tile
+  if (sh.rt_shift == 4) {
+    const long long rows = ((long long)M * p.G + batch - 1) / batch;
+    return launch_pdl(f32 ? attn_join_kernel<true, false> : attn_join_kernel<false, false>,
+                      dim3((unsigned)p.target, (unsigned)std::min(rows, 16ll)),
+                      dim3(kAttnThreads), 0, st, p);
+  }
+  return launch_pdl(f32 ? attn_join_kernel<true, true> : attn_join_kernel<false, true>,
+                    dim3((unsigned)p.target, (1u << sh.rt_shift) / 32), dim3(kAttnThreads), 0, st,
+                    p);
 }
 
 const char* bitnet_last_error(void) { return g_last_error.c_str(); }
