@@ -90,6 +90,15 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// 32 lanes x 8 columns of 32-bit TMEM -> registers.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+
 // registers -> 32 lanes x 16 columns of 32-bit TMEM.
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -466,31 +475,29 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
           part[row] = m;
           part[C::RT + row] = l;
         }
-#pragma unroll 1
-        for (int d = 0; d < DP; d += 32) {
-          uint32_t o[32];
+        // The rows leave through the Q tile, which is done with, so that a warp
+        // stores whole rows: W columns at a time, bf16 or fp32 sums.
+        auto columns = [&](int d, float (&x)[8]) {
+          uint32_t o[8];
           if (job.cnt[t] > 0) {
-            tmem_ld_32x32b_x32(ocol + d, o);
+            tmem_ld_32x32b_x8(ocol + d, o);
             tmem_ld_wait();
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0u;
+            for (int k = 0; k < 8; ++k) o[k] = 0u;
           }
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[k + e]) * inv;
-            if (job.q.slot >= 0) {
-              if (live && d + k < D) store_f32<8>(part + 2 * C::RT + (long long)row * D + d + k, x);
-            } else {                             // through the Q tile, which is done with
-              store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(
-                                smem + t * C::TILE + ((d + k) >> 6) * C::SUB + r * 128 +
-                                ((((d + k) >> 3 & 7) ^ (r & 7)) << 4)), x);
-            }
-          }
-        }
+          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[k]) * inv;
+        };
         if (job.q.slot < 0) {
+#pragma unroll 4
+          for (int d = 0; d < DP; d += 8) {
+            float x[8];
+            columns(d, x);
+            store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(
+                              smem + t * C::TILE + (d >> 6) * C::SUB + r * 128 +
+                              (((d >> 3 & 7) ^ (r & 7)) << 4)), x);
+          }
           __syncwarp();
           each_row([&](int k, long long off) {
             const int rr = wrow + sub + STEP * k;
@@ -499,6 +506,31 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
                   *reinterpret_cast<const uint4*>(qtile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
           });
           __syncwarp();
+        } else {
+          constexpr int W = C::TILE / 512, RB = 4 * W;       // columns, bytes of a staged row
+          constexpr int WL = W / 4, WSTEP = 32 / WL;         // lanes per row, rows at a time
+          uint8_t* st = smem + t * C::TILE;
+#pragma unroll 1
+          for (int d0 = 0; d0 < DP; d0 += W) {
+#pragma unroll 4
+            for (int d = 0; d < W; d += 8) {
+              float x[8];
+              columns(d0 + d, x);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float4*>(st + r * RB + (((d / 4 + e) ^ (r & 7)) << 4)) =
+                    make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
+            __syncwarp();
+            const int wch = lane % WL, d = d0 + 4 * wch;
+#pragma unroll 4
+            for (int rr = wrow + lane / WL; rr < wrow + 32; rr += WSTEP) {
+              if (128 * t + rr < job.q.nrows && d < D)
+                *reinterpret_cast<float4*>(part + 2 * C::RT + (long long)(128 * t + rr) * D + d) =
+                    *reinterpret_cast<const float4*>(st + rr * RB + ((wch ^ (rr & 7)) << 4));
+            }
+            __syncwarp();
+          }
         }
       }
       tc_fence_before();
