@@ -262,6 +262,12 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// An 8 x 8 matrix of 16-bit values, one row per four lanes, transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -270,9 +276,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 // ------------------------------------------------------- mma.sync kernel
 // Four warps: WR of them along the rows (16 each), 4 / WR along the keys of a
-// block.  WR = 1 is the decode form: 16 rows, each warp its own quarter of
-// every block with its own statistics, joined in shared memory at the end.
-// WR = 4 takes 64 rows of a chunk.
+// block.  WR = 1 takes up to 16 rows, each warp its own quarter of every block
+// with its own statistics, joined in shared memory at the end.  WR = 4 takes
+// 64 rows of a chunk.  WR = 0 is the decode form: 8 rows, the four warps along
+// the keys, and both products transposed (keys and head elements are the 16
+// rows of the matrix instruction, the query rows its 8 columns), which halves
+// the instructions and registers where most of 16 rows would be padding.
 //
 // fp32 queries (F32): q and the probabilities are held as three bf16 terms (24
 // bits, exact), so their products with the bf16 cache are those of fp32, for
@@ -282,8 +291,8 @@ __device__ __forceinline__ float ex2(float x) {
 // the keys, below the rounding of the output); l sums the unrounded ones.
 template <int DP, int WR, bool F32>
 struct AttnConfig {
-  static constexpr int RT = 16 * WR;
-  static constexpr int WK = 4 / WR;
+  static constexpr int RT = WR == 0 ? 8 : 16 * WR;
+  static constexpr int WK = WR == 4 ? 1 : 4;
   static constexpr int KW = kAttnTile / WK;          // keys of a warp per block
   static constexpr int STAGES = DP == 64 ? 4 : DP == 128 ? 3 : 2;
   static constexpr int TERMS = F32 ? 3 : 1;
@@ -294,7 +303,7 @@ struct AttnConfig {
   static constexpr int OFF_KV = Q_BYTES;
   static constexpr int OFF_PAGES = OFF_KV + STAGES * 2 * KV_BYTES;
   static constexpr int SMEM = OFF_PAGES + PAGE_TILES * (kAttnTile / 16) * 8;
-  static constexpr bool Q_REGS = !F32 && DP <= 128;
+  static constexpr bool Q_REGS = WR > 0 && !F32 && DP <= 128;
   static_assert(WK * RT * DP * 4 <= STAGES * 2 * KV_BYTES || WR == 4, "join buffer");
 };
 
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
   const uint32_t sq = smem_u32(attn_smem), skv = sq + C::OFF_KV;
   long long* s_off = reinterpret_cast<long long*>(attn_smem + C::OFF_PAGES);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wr = WR == 1 ? 0 : warp, wk = WR == 1 ? warp : 0;
+  const int wr = WR == 4 ? warp : 0, wk = WR == 4 ? 0 : warp;
   const int D = p.D, chunks = D / 8;
 
   grid_launch_dependents();
@@ -422,19 +431,21 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
 #pragma unroll 1
     for (int i = 0; i < C::STAGES - 1; ++i) load(i);
 
-    float o[DP / 8][4];
+    constexpr int OT = WR == 0 ? DP / 16 : DP / 8;   // accumulator tiles
+    float o[OT][4];
 #pragma unroll
-    for (int i = 0; i < DP / 8; ++i)
+    for (int i = 0; i < OT; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     int lim[2];                                      // keys that this thread's rows see
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int r = 16 * wr + (lane >> 2) + 8 * k;
+      const int r = WR == 0 ? 2 * (lane & 3) + k : 16 * wr + (lane >> 2) + 8 * k;
       lim[k] = r < nrows ? past + (row0 + r) / p.G + 1 : 0;
     }
     uint32_t qf[C::Q_REGS ? DP / 16 : 1][4];
+    uint32_t qt[WR == 0 ? C::TERMS : 1][WR == 0 ? DP / 32 : 1][4];   // transposed: two steps each
 
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
@@ -447,124 +458,207 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
             ldmatrix_x4(attn_at<C::ROW>(sq, 16 * wr + (lane & 15), 2 * k + (lane >> 4)), qf[k]);
         }
       }
+      if constexpr (WR == 0) {
+        if (i == 0) {
+#pragma unroll
+          for (int t = 0; t < C::TERMS; ++t)
+#pragma unroll
+            for (int k = 0; k < DP / 32; ++k)
+              ldmatrix_x4(attn_at<C::ROW>(sq + t * C::RT * C::ROW, lane & 7, 4 * k + (lane >> 3)),
+                          qt[t][k]);
+        }
+      }
       load(i + C::STAGES - 1);
       const uint32_t sk = skv + (uint32_t)((i % C::STAGES) * 2 * C::KV_BYTES);
       const uint32_t sv = sk + C::KV_BYTES;
-      float z[C::KW / 8][4];
+      if constexpr (WR == 0) {
+        // scores: rows are this warp's 16 keys, columns the query rows; two
+        // chains of products, so that one's latency hides the other's
+        float z0[4] = {0, 0, 0, 0}, z1[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int n = 0; n < C::KW / 8; ++n)
+        for (int k = 0; k < DP / 16; ++k) {
+          uint32_t a[4];
+          ldmatrix_x4(attn_at<C::ROW>(sk, 16 * wk + (lane & 15), 2 * k + (lane >> 4)), a);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) z[n][k] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < DP / 16; ++k) {
-        uint32_t a[C::TERMS][4];
-        if constexpr (C::Q_REGS) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) a[0][x] = qf[k][x];
-        } else {
-#pragma unroll
-          for (int t = 0; t < C::TERMS; ++t)
-            ldmatrix_x4(attn_at<C::ROW>(sq + t * C::RT * C::ROW, 16 * wr + (lane & 15),
-                                        2 * k + (lane >> 4)), a[t]);
+          for (int t = C::TERMS - 1; t >= 0; --t)    // smallest terms first
+            mma_bf16((k & 1) ? z1 : z0, a, qt[t][k / 2][2 * (k & 1)], qt[t][k / 2][2 * (k & 1) + 1]);
         }
-#pragma unroll
-        for (int n = 0; n < C::KW / 16; ++n) {
-          uint32_t kb[4];
-          ldmatrix_x4(attn_at<C::ROW>(sk, C::KW * wk + 16 * n + (lane & 7) + ((lane >> 4) << 3),
-                                      2 * k + ((lane >> 3) & 1)), kb);
-#pragma unroll
-          for (int t = C::TERMS - 1; t >= 0; --t) {  // smallest terms first
-            mma_bf16(z[2 * n], a[t], kb[0], kb[1]);
-            mma_bf16(z[2 * n + 1], a[t], kb[2], kb[3]);
-          }
-        }
-      }
-      const int key0 = (blk0 + i) * kAttnTile + C::KW * wk + 2 * (lane & 3);
-      const bool masked = (blk0 + i + 1) * kAttnTile > lim_first || nrows < C::RT;
-      float mx[2] = {m[0], m[1]};
-#pragma unroll
-      for (int n = 0; n < C::KW / 8; ++n)
+        const int key = (blk0 + i) * kAttnTile + 16 * wk + (lane >> 2);
+        const bool masked = (blk0 + i + 1) * kAttnTile > lim_first || nrows < C::RT;
+        float mx[2] = {m[0], m[1]};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float v = z[n][k] * p.scale_log2;
-          if (masked && key0 + 8 * n + (k & 1) >= lim[k >> 1]) v = -INFINITY;
-          z[n][k] = v;
-          mx[k >> 1] = fmaxf(mx[k >> 1], v);
+          z0[k] = (z0[k] + z1[k]) * p.scale_log2;
+          if (masked && key + 8 * (k >> 1) >= lim[k & 1]) z0[k] = -INFINITY;
+          mx[k & 1] = fmaxf(mx[k & 1], z0[k]);
         }
-      float alpha[2], base[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-        base[k] = mx[k] == -INFINITY ? 0.0f : mx[k];  // nothing seen yet: all terms are 0
-        alpha[k] = ex2(m[k] - base[k]);
-        m[k] = mx[k];
-        l[k] *= alpha[k];
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+        for (int x = 4; x < 32; x *= 2)
 #pragma unroll
-        for (int n = 0; n < DP / 8; ++n) {
-          o[n][0] *= alpha[0];
-          o[n][1] *= alpha[0];
-          o[n][2] *= alpha[1];
-          o[n][3] *= alpha[1];
+          for (int k = 0; k < 2; ++k)
+            mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], x));
+        float alpha[2], base[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          base[k] = mx[k] == -INFINITY ? 0.0f : mx[k];   // nothing seen yet: all terms are 0
+          alpha[k] = ex2(m[k] - base[k]);
+          m[k] = mx[k];
+          l[k] *= alpha[k];
         }
-      }
-      uint32_t pf[C::KW / 16][C::TERMS][4];          // the probabilities' terms
+        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
 #pragma unroll
-      for (int n = 0; n < C::KW / 16; ++n) {
-        float e[8];
+          for (int n = 0; n < OT; ++n)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          e[k] = ex2(z[2 * n + (k >> 2)][k & 3] - base[(k >> 1) & 1]);
-          l[(k >> 1) & 1] += e[k];
+            for (int k = 0; k < 4; ++k) o[n][k] *= alpha[k & 1];
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          z0[k] = ex2(z0[k] - base[k & 1]);
+          l[k & 1] += z0[k];
+        }
+        uint32_t pb[C::TERMS][2];                    // probabilities, keys along the pairs
 #pragma unroll
         for (int t = 0; t < C::TERMS; ++t)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            pf[n][t][k] = pack_bf16x2(e[2 * k], e[2 * k + 1]);
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w2 = pack_bf16x2(z0[2 * k], z0[2 * k + 1]);
             if constexpr (F32) {
-              e[2 * k] -= __uint_as_float(pf[n][t][k] << 16);
-              e[2 * k + 1] -= __uint_as_float(pf[n][t][k] & 0xffff0000u);
+              z0[2 * k] -= __uint_as_float(w2 << 16);
+              z0[2 * k + 1] -= __uint_as_float(w2 & 0xffff0000u);
+            }
+            pb[t][k] = movmatrix_trans(w2);
+          }
+#pragma unroll
+        for (int d = 0; d < OT; ++d) {
+          uint32_t a[4];
+          ldmatrix_x4_trans(attn_at<C::ROW>(sv, 16 * wk + (lane & 7) + ((lane >> 4) << 3),
+                                            2 * d + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
+          if constexpr (F32) {                       // a block's sum is added rounded, see below
+            float t0[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int t = C::TERMS - 1; t >= 0; --t) mma_bf16(t0, a, pb[t][0], pb[t][1]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[d][k] += t0[k];
+          } else {
+            mma_bf16(o[d], a, pb[0][0], pb[0][1]);
+          }
+        }
+      } else {
+        float z[C::KW / 8][4];
+#pragma unroll
+        for (int n = 0; n < C::KW / 8; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z[n][k] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          uint32_t a[C::TERMS][4];
+          if constexpr (C::Q_REGS) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) a[0][x] = qf[k][x];
+          } else {
+#pragma unroll
+            for (int t = 0; t < C::TERMS; ++t)
+              ldmatrix_x4(attn_at<C::ROW>(sq + t * C::RT * C::ROW, 16 * wr + (lane & 15),
+                                          2 * k + (lane >> 4)), a[t]);
+          }
+#pragma unroll
+          for (int n = 0; n < C::KW / 16; ++n) {
+            uint32_t kb[4];
+            ldmatrix_x4(attn_at<C::ROW>(sk, C::KW * wk + 16 * n + (lane & 7) + ((lane >> 4) << 3),
+                                        2 * k + ((lane >> 3) & 1)), kb);
+#pragma unroll
+            for (int t = C::TERMS - 1; t >= 0; --t) {  // smallest terms first
+              mma_bf16(z[2 * n], a[t], kb[0], kb[1]);
+              mma_bf16(z[2 * n + 1], a[t], kb[2], kb[3]);
             }
           }
-      }
-#pragma unroll
-      for (int d = 0; d < DP / 16; ++d) {
-        // fp32: a block's sum starts at zero and is added rounded, since a
-        // matrix instruction truncates its running sum (over thousands of
-        // keys that came to 1.6e-6)
-        float t0[4], t1[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          t0[k] = F32 ? 0.0f : o[2 * d][k];
-          t1[k] = F32 ? 0.0f : o[2 * d + 1][k];
         }
+        const int key0 = (blk0 + i) * kAttnTile + C::KW * wk + 2 * (lane & 3);
+        const bool masked = (blk0 + i + 1) * kAttnTile > lim_first || nrows < C::RT;
+        float mx[2] = {m[0], m[1]};
 #pragma unroll
-        for (int n = 0; n < C::KW / 16; ++n) {
-          uint32_t v0, v1, v2, v3;
-          ldmatrix_x4_trans(attn_at<C::ROW>(sv, C::KW * wk + 16 * n + (lane & 15),
-                                            2 * d + (lane >> 4)), v0, v1, v2, v3);
+        for (int n = 0; n < C::KW / 8; ++n)
 #pragma unroll
-          for (int t = C::TERMS - 1; t >= 0; --t) {
-            mma_bf16(t0, pf[n][t], v0, v1);
-            mma_bf16(t1, pf[n][t], v2, v3);
+          for (int k = 0; k < 4; ++k) {
+            float v = z[n][k] * p.scale_log2;
+            if (masked && key0 + 8 * n + (k & 1) >= lim[k >> 1]) v = -INFINITY;
+            z[n][k] = v;
+            mx[k >> 1] = fmaxf(mx[k >> 1], v);
+          }
+        float alpha[2], base[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+          base[k] = mx[k] == -INFINITY ? 0.0f : mx[k];  // nothing seen yet: all terms are 0
+          alpha[k] = ex2(m[k] - base[k]);
+          m[k] = mx[k];
+          l[k] *= alpha[k];
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+          for (int n = 0; n < DP / 8; ++n) {
+            o[n][0] *= alpha[0];
+            o[n][1] *= alpha[0];
+            o[n][2] *= alpha[1];
+            o[n][3] *= alpha[1];
           }
         }
+        uint32_t pf[C::KW / 16][C::TERMS][4];          // the probabilities' terms
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          o[2 * d][k] = F32 ? o[2 * d][k] + t0[k] : t0[k];
-          o[2 * d + 1][k] = F32 ? o[2 * d + 1][k] + t1[k] : t1[k];
+        for (int n = 0; n < C::KW / 16; ++n) {
+          float e[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            e[k] = ex2(z[2 * n + (k >> 2)][k & 3] - base[(k >> 1) & 1]);
+            l[(k >> 1) & 1] += e[k];
+          }
+#pragma unroll
+          for (int t = 0; t < C::TERMS; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              pf[n][t][k] = pack_bf16x2(e[2 * k], e[2 * k + 1]);
+              if constexpr (F32) {
+                e[2 * k] -= __uint_as_float(pf[n][t][k] << 16);
+                e[2 * k + 1] -= __uint_as_float(pf[n][t][k] & 0xffff0000u);
+              }
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+          // fp32: a block's sum starts at zero and is added rounded, since a
+          // matrix instruction truncates its running sum (over thousands of
+          // keys that came to 1.6e-6)
+          float t0[4], t1[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            t0[k] = F32 ? 0.0f : o[2 * d][k];
+            t1[k] = F32 ? 0.0f : o[2 * d + 1][k];
+          }
+#pragma unroll
+          for (int n = 0; n < C::KW / 16; ++n) {
+            uint32_t v0, v1, v2, v3;
+            ldmatrix_x4_trans(attn_at<C::ROW>(sv, C::KW * wk + 16 * n + (lane & 15),
+                                              2 * d + (lane >> 4)), v0, v1, v2, v3);
+#pragma unroll
+            for (int t = C::TERMS - 1; t >= 0; --t) {
+              mma_bf16(t0, pf[n][t], v0, v1);
+              mma_bf16(t1, pf[n][t], v2, v3);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[2 * d][k] = F32 ? o[2 * d][k] + t0[k] : t0[k];
+            o[2 * d + 1][k] = F32 ? o[2 * d + 1][k] + t1[k] : t1[k];
+          }
         }
       }
     }
     cp_async_wait<0>();
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
-      l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-    }
+    for (int x = WR == 0 ? 4 : 1; x < (WR == 0 ? 32 : 4); x *= 2)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) l[k] += __shfl_xor_sync(0xffffffffu, l[k], x);
 
     float* part = slot >= 0 ? p.part + (long long)slot * C::RT * (D + 2) : nullptr;
     auto store2 = [&](int r, int d, float x, float y) {
@@ -581,34 +675,42 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
         *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.O) + off) =
             pack_bf16x2(x, y);
     };
-    if constexpr (WR == 1) {
+    if constexpr (WR <= 1) {
       // the four warps' sums, each relative to the rows' common maximum
       __syncthreads();                               // the ring is free
-      if ((lane & 3) == 0) {
+      if (WR == 0 ? lane < 4 : (lane & 3) == 0) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          s_m[warp][(lane >> 2) + 8 * k] = m[k];
-          s_l[warp][(lane >> 2) + 8 * k] = l[k];
+          const int r = WR == 0 ? 2 * lane + k : (lane >> 2) + 8 * k;
+          s_m[warp][r] = m[k];
+          s_l[warp][r] = l[k];
         }
       }
       __syncthreads();
-      float* so = reinterpret_cast<float*>(attn_smem + C::OFF_KV);   // [4][16][DP]
+      float* so = reinterpret_cast<float*>(attn_smem + C::OFF_KV);   // [4][RT][DP]
       float f[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int r = (lane >> 2) + 8 * k;
+        const int r = WR == 0 ? 2 * (lane & 3) + k : (lane >> 2) + 8 * k;
         const float mm = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
         f[k] = mm == -INFINITY ? 0.0f : ex2(m[k] - mm);
       }
 #pragma unroll
-      for (int n = 0; n < DP / 8; ++n)
+      for (int n = 0; n < OT; ++n) {
+        if constexpr (WR == 0) {
+          float* x = so + (warp * C::RT + 2 * (lane & 3)) * DP + 16 * n + (lane >> 2);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          *reinterpret_cast<float2*>(so + (warp * 16 + (lane >> 2) + 8 * k) * DP + 8 * n +
-                                     2 * (lane & 3)) =
-              make_float2(o[n][2 * k] * f[k], o[n][2 * k + 1] * f[k]);
+          for (int k = 0; k < 4; ++k) x[(k & 1) * DP + 8 * (k >> 1)] = o[n][k] * f[k & 1];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float2*>(so + (warp * C::RT + (lane >> 2) + 8 * k) * DP + 8 * n +
+                                       2 * (lane & 3)) =
+                make_float2(o[n][2 * k] * f[k], o[n][2 * k + 1] * f[k]);
+        }
+      }
       __syncthreads();
-      for (int i = tid; i < 16 * (D / 2); i += kAttnThreads) {
+      for (int i = tid; i < C::RT * (D / 2); i += kAttnThreads) {
         const int r = i / (D / 2), d = 2 * (i % (D / 2));
         if (r >= nrows) break;
         const float mm = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
@@ -616,7 +718,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           sum += mm == -INFINITY ? 0.0f : s_l[q][r] * ex2(s_m[q][r] - mm);
-          const float2 v = *reinterpret_cast<const float2*>(so + (q * 16 + r) * DP + d);
+          const float2 v = *reinterpret_cast<const float2*>(so + (q * C::RT + r) * DP + d);
           x += v.x;
           y += v.y;
         }

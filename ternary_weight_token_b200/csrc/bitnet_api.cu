@@ -878,11 +878,13 @@ AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, 
                      float scale) {
   const int G = q_heads / kv_heads;
   AttnShape sh = {};
-  // Up to 16 rows per sequence on average: tiles of 16, the keys of a block
-  // shared out to four warps.  Above, the tensor-core kernel's pairs of
-  // 128-row tiles for bf16; its softmax wants a positive scale.  What is left
-  // takes tiles of 64, heads wider than 128 (no registers for 64) of 16.
-  const bool few = (long long)M * G <= 16ll * batch;
+  // Up to 8 rows per sequence on average: tiles of 8, up to 16: tiles of 16,
+  // the keys of a block shared out to four warps.  Above, the tensor-core
+  // kernel's pairs of 128-row tiles for bf16; its softmax wants a positive
+  // scale.  What is left takes tiles of 64, heads wider than 128 (no registers
+  // for 64) of 16.
+  const long long rows = (long long)M * G;
+  const bool few = rows <= 16ll * batch;
   sh.tc = !few && !f32 && head_dim <= 128 && scale > 0.0f;
   if (sh.tc) {
     sh.rt_shift = 8;
@@ -890,9 +892,9 @@ AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, 
     sh.min_units = 3;
     sh.target = kAttnTcTarget;
   } else {
-    sh.rt_shift = few || head_dim > 128 ? 4 : 6;
+    sh.rt_shift = rows <= 8ll * batch ? 3 : few || head_dim > 128 ? 4 : 6;
     sh.unit_shift = 6;
-    sh.min_units = sh.rt_shift == 4 ? 2 : 8;
+    sh.min_units = sh.rt_shift <= 4 ? 2 : 8;
     sh.target = kAttnTarget;
   }
   // enough items to deal out whole
@@ -945,7 +947,7 @@ template <int WR, bool F32>
 int launch_attn_dim(AttnParams& p, int sms, cudaStream_t st) {
   if (p.D <= 64) return launch_attn_rows<64, WR, F32>(p, sms, st);
   if (p.D <= 128) return launch_attn_rows<128, WR, F32>(p, sms, st);
-  if constexpr (WR == 1) return launch_attn_rows<256, WR, F32>(p, sms, st);
+  if constexpr (WR <= 1) return launch_attn_rows<256, WR, F32>(p, sms, st);
   return BITNET_ERR_UNSUPPORTED;                     // attn_shape() keeps these at 16 rows
 }
 
@@ -1662,6 +1664,8 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   int rc;
   if (sh.tc)
     rc = head_dim <= 64 ? launch_attn_tc<64>(p, di.sms, st) : launch_attn_tc<128>(p, di.sms, st);
+  else if (sh.rt_shift == 3)
+    rc = f32 ? launch_attn_dim<0, true>(p, di.sms, st) : launch_attn_dim<0, false>(p, di.sms, st);
   else if (sh.rt_shift == 4)
     rc = f32 ? launch_attn_dim<1, true>(p, di.sms, st) : launch_attn_dim<1, false>(p, di.sms, st);
   else
@@ -1669,7 +1673,7 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   if (rc || p.target == 0) return rc;
   // a CTA per share, and per row of its item (16 rows at most, or that many
   // per sequence on average), or per 32 rows of a wide tile
-  if (sh.rt_shift == 4) {
+  if (sh.rt_shift <= 4) {
     const long long rows = ((long long)M * p.G + batch - 1) / batch;
     return launch_pdl(f32 ? attn_join_kernel<true, false> : attn_join_kernel<false, false>,
                       dim3((unsigned)p.target, (unsigned)std::min(rows, 16ll)),
