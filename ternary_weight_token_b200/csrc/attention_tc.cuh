@@ -23,8 +23,6 @@
 //                   slots hold, 0 x NaN must not reach the sums)
 #pragma once
 
-#include <type_traits>
-
 #include "attention.cuh"
 #include "common.cuh"
 
@@ -136,32 +134,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// 2^x of two finite values on the fp32 pipe instead of the exponential unit
-// (16 results per cycle and SM, which bounds the softmax): n = rint(x), a cubic
-// in f = x - n on [-1/2, 1/2] (minimax in the relative error by
-// Remez exchange, 7.5e-5: a fiftieth of the bf16 rounding that follows), n added to the exponent.
-__device__ __forceinline__ void ex2_poly2(uint64_t z, float& x, float& y) {
-  constexpr float kRound = 12582912.0f;          // 1.5 * 2^23: the sum's low bits are n
-  constexpr float c0 = 0.99992807f, c1 = 0.69326099f, c2 = 0.24261112f, c3 = 0.05517167f;
-  unpack_f32x2(z, x, y);
-  z = pack_f32x2(fmaxf(x, -126.0f), fmaxf(y, -126.0f));
-  const uint64_t n = add_f32x2(z, pack_f32x2(kRound, kRound));
-  const uint64_t f =
-      fma_f32x2(add_f32x2(n, pack_f32x2(-kRound, -kRound)), pack_f32x2(-1.0f, -1.0f), z);
-  uint64_t r = fma_f32x2(f, pack_f32x2(c3, c3), pack_f32x2(c2, c2));
-  r = fma_f32x2(f, r, pack_f32x2(c1, c1));
-  r = fma_f32x2(f, r, pack_f32x2(c0, c0));
-  float u, v;
-  unpack_f32x2(r, x, y);
-  unpack_f32x2(n, u, v);
-  x = __int_as_float(__float_as_int(x) + (__float_as_int(u) << 23));
-  y = __int_as_float(__float_as_int(y) + (__float_as_int(v) << 23));
-}
-
 constexpr int kAttnTcThreads = 384;
 constexpr int kAttnTcTarget = 148;     // most shares of a call: one per SM
 constexpr int kAttnTcKeys = 128;       // keys per block
-constexpr int kAttnTcPoly = 4;         // every fourth pair of powers on the fp32 pipe
 constexpr float kAttnTcLazy = 8.0f;    // growth of a row's maximum that rescales O
 
 constexpr int kAttnTcList = 8;         // items laid out at a time
@@ -178,7 +153,7 @@ struct AttnTcConfig {
   static constexpr int HALVES = DP / 64;                     // 64-column sub-tiles
   static constexpr int SUB = 128 * 128;                      // bytes of one
   static constexpr int TILE = HALVES * SUB;                  // Q tile, K or V block
-  static constexpr int SLOTS = DP == 128 ? 5 : 8;
+  static constexpr int SLOTS = DP == 128 ? 4 : 8;            // five were no faster than four
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
   static constexpr int NUM_BARS = 2 * SLOTS + 16;
@@ -306,8 +281,9 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
     }
   };
 
+  // 256 x 224 + 128 x 56 registers: the 384 x 168 of the launch
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     walk([&](const AttnTcItem& job) {
       // --------------------------------------------------------- softmax
       const int t = warp >> 2, r = threadIdx.x & 127;        // tile and row in it
@@ -373,8 +349,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(scol + 32u * q, s[q]);
         tmem_ld_wait();
         const int key0 = (job.q.blk0 + i) * kAttnTcKeys;
-        const bool masked = key0 + kAttnTcKeys > lim_warp;
-        if (masked) {
+        if (key0 + kAttnTcKeys > lim_warp) {
           const int n = lim - key0;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -401,7 +376,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
         uint64_t lh = 0;
         uint32_t ph[32];
-        auto powers = [&](int half, float base, auto all_seen) {
+        auto powers = [&](int half, float base) {
           const uint64_t base2 = pack_f32x2(base, base);
           lh = 0;
 #pragma unroll
@@ -410,13 +385,9 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
             const uint64_t z = fma_f32x2(
                 pack_f32x2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), scale2, base2);
             float u, v;
-            if (decltype(all_seen)::value && k % kAttnTcPoly == kAttnTcPoly - 1) {
-              ex2_poly2(z, u, v);
-            } else {
-              unpack_f32x2(z, u, v);
-              u = ex2(u);
-              v = ex2(v);
-            }
+            unpack_f32x2(z, u, v);
+            u = ex2(u);
+            v = ex2(v);
             lh = add_f32x2(lh, pack_f32x2(u, v));
             ph[k] = pack_bf16x2(u, v);
           }
@@ -429,37 +400,31 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&pfull[2 * t + half]);
         };
-        auto block = [&](auto all_seen) {
-          float base = m == -INFINITY ? 0.0f : -m;
-          powers(0, base, all_seen);
-          const bool grow = mnew > m + kAttnTcLazy || (m == -INFINITY && mnew != -INFINITY);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? ex2(m - mnew) : 1.0f;
-            l2 = fma_f32x2(l2, pack_f32x2(f, f), 0);
-            if (grow) m = mnew;
-            base = m == -INFINITY ? 0.0f : -m;
-            // the product of the last block is done: its completion precedes
-            // that of the scores just read
+        float base = m == -INFINITY ? 0.0f : -m;
+        powers(0, base);
+        const bool grow = mnew > m + kAttnTcLazy || (m == -INFINITY && mnew != -INFINITY);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2(m - mnew) : 1.0f;
+          l2 = fma_f32x2(l2, pack_f32x2(f, f), 0);
+          if (grow) m = mnew;
+          base = m == -INFINITY ? 0.0f : -m;
+          // the product of the last block is done: its completion precedes
+          // that of the scores just read
 #pragma unroll 1
-            for (int d = 0; d < DP; d += 16) {
-              uint32_t o[16];
-              tmem_ld_32x32b_x16(ocol + d, o);
-              tmem_ld_wait();
+          for (int d = 0; d < DP; d += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(ocol + d, o);
+            tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st_32x32b_x16(ocol + d, o);
-            }
-            tmem_st_wait();
-            powers(0, base, all_seen);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st_32x32b_x16(ocol + d, o);
           }
-          hand_over(0);
-          powers(1, base, all_seen);
-          hand_over(1);
-        };
-        if (masked)
-          block(std::false_type{});
-        else
-          block(std::true_type{});
+          tmem_st_wait();
+          powers(0, base);
+        }
+        hand_over(0);
+        powers(1, base);
+        hand_over(1);
       }
       // ---- the rows' sums
       float l, lb;
@@ -536,7 +501,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       tc_fence_before();
     });
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 8) {
       walk([&](const AttnTcItem& job) {
       // -------------------------------------------------------- producer
@@ -595,13 +560,16 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         const uint32_t done0 = t == 0 ? blocks_done[0] : blocks_done[1];
         const int both = min(job.cnt[0], job.cnt[1]);
         const bool last_here = cnt == job.count && (t == 1 || job.cnt[1] < job.count);
-        auto scores = [&](uint32_t st) {
+        // pass: hand the turn over half way, since it takes the other issuer
+        // about as long as the second half to notice
+        auto scores = [&](uint32_t st, bool pass) {
           const uint64_t kd = make_sdesc_sw128(kva + st * C::TILE);
           if (leader) {
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
               const uint64_t o = (uint64_t)((k >> 2) * (C::SUB >> 4) + 2 * (k & 3));
               mma_f16_ss(scol, qd + o, kd + o, idesc_s, k != 0);
+              if (k == DP / 32 - 1 && pass) mbar_arrive(&turn[1 - t]);
             }
             tc_commit(&sfull[t]);
             tc_commit(&empty[st]);
@@ -614,7 +582,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (ok && cnt > 0) {
           tc_fence_after();
-          scores(it % C::SLOTS);
+          scores(it % C::SLOTS, false);
         } else if (ok && lane == 0) {
           mbar_arrive(&empty[it % C::SLOTS]);
         }
@@ -672,14 +640,14 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
               tc_fence_after();
-              scores(sk);
+              scores(sk, turns);
             }
           } else if (more) {
             ok = ok && mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (ok && lane == 0) mbar_arrive(&empty[sk]);
           }
-          if (ok && turns && leader) mbar_arrive(&turn[1 - t]);
+          if (ok && turns && leader && !(more && i + 1 < cnt)) mbar_arrive(&turn[1 - t]);
         }
       }
       __syncwarp();
