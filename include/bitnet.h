@@ -445,8 +445,9 @@ BITNET_API int bitnet_ffn_noalloc(const void *X, int x_dtype, int M, int H, int 
 BITNET_API const char *bitnet_last_error(void);
 
 /* Synchronise `stream`, then read and clear the device error word.  Returns
- * BITNET_OK, BITNET_ERR_TIMEOUT (a bounded wait inside a kernel gave up) or
- * BITNET_ERR_CUDA.  Debug / test call: it blocks the host. */
+ * BITNET_OK, BITNET_ERR_TIMEOUT (a bounded wait inside a kernel gave up),
+ * BITNET_ERR_INVALID_ARG (a page index, row or length in device memory was out
+ * of range) or BITNET_ERR_CUDA.  Debug / test call: it blocks the host. */
 BITNET_API int bitnet_check_device_error(bitnet_stream_t stream);
 
 /* Diagnostic: launch one block that waits on a barrier no thread ever

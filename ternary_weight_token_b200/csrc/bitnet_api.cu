@@ -1638,6 +1638,7 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   for (const void* q : words)
     if (reinterpret_cast<uintptr_t>(q) & 3u)
       return fail(BITNET_ERR_INVALID_ARG, "tables must be 4-byte aligned");
+  if (O == Q) return fail(BITNET_ERR_INVALID_ARG, "O must not be Q's buffer");
   const size_t ws_need = bitnet_attention_workspace_size(M, batch, q_heads, kv_heads, head_dim);
   if (workspace == nullptr || ws_bytes < ws_need)
     return fail(BITNET_ERR_WORKSPACE, "workspace of %zu bytes needed", ws_need);

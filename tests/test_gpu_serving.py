@@ -118,6 +118,84 @@ def test_attention_large_scores_keep_the_running_maximum():
         close(got, o, ref.attention_tolerance(BF, o, a, smax, 64), "attention")
 
 
+@pytest.mark.parametrize("D", [16, 48, 80, 112])
+@pytest.mark.parametrize("page", [16, 48, 256])
+def test_attention_chunks_of_other_head_widths(D, page):
+    check_attention([(70, 170), (31, 31), (1, 400)], 6, 2, D, page, BF)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_long_history_of_a_chunk(dtype):
+    """Few items over many keys: every one is cut into many shares."""
+    check_attention([(40, 20011)], 8, 8, 64, 32, dtype)
+    check_attention([(9, 6000), (90, 133)], 20, 1, 96, 16, dtype)
+
+
+def test_attention_ten_new_tokens_each():
+    """More than 16 rows a sequence, all in one tile; then 9 to 16 rows."""
+    check_attention([(10, 500)] * 7, 20, 5, 128, 16, BF)
+    check_attention([(3, 500 + 7 * i) for i in range(9)], 20, 5, 128, 16, BF)
+    check_attention([(3, 500 + 7 * i) for i in range(9)], 20, 5, 128, 16, F32)
+
+
+@pytest.mark.parametrize("n", [1, 3, 90])
+def test_offsets_past_32_bits(n):
+    """Pages whose elements lie past 2^31 in the caches."""
+    kvh, D, page, qh = 5, 128, 16, 20
+    pages = 2 ** 31 // (kvh * page * D) + 40
+    s = ref.batch([(n, 300)], page, kvh, D, seed=12, spare=0)
+    q, k, v = (torch.randn(n, h * D, generator=s["g"]).to(BF) for h in (qh, kvh, kvh))
+    inv = torch.rand(D // 2, generator=s["g"])
+    d = cuda(s)
+    used = s["kc"].shape[0]
+    big = {}
+    for key in ("kc", "vc"):
+        big[key] = torch.empty(pages, kvh, page, D, dtype=BF, device="cuda")
+        big[key][pages - used:] = d[key]
+    table = torch.where(d["table"] >= 0, d["table"] + (pages - used), d["table"])
+    small_q, big_q = torch.empty_like(q, device="cuda"), torch.empty_like(q, device="cuda")
+    args = (q.cuda(), k.cuda(), v.cuda(), inv.cuda(), d["cu"], d["len"])
+    bn.bitnet_rope_append(*args, d["table"], d["kc"], d["vc"], small_q)
+    bn.bitnet_rope_append(*args, table, big["kc"], big["vc"], big_q)
+    assert torch.equal(small_q, big_q)
+    for key in ("kc", "vc"):
+        assert torch.equal(big[key][pages - used:], d[key])
+    ws = bn.alloc_attention_workspace(n, 1, qh, kvh, D)
+    o1, o2 = torch.empty_like(small_q), torch.empty_like(small_q)
+    bn.bitnet_attention(small_q, d["cu"], d["len"], d["table"], d["kc"], d["vc"], o1, ws)
+    bn.bitnet_attention(big_q, d["cu"], d["len"], table, big["kc"], big["vc"], o2, ws)
+    assert torch.equal(o1, o2)
+    assert bn.bitnet_check_device_error() == bn.BITNET_OK
+    now = {**s, "kc": d["kc"].cpu(), "vc": d["vc"].cpu()}
+    want, a, smax = ref.attention(now, small_q.cpu(), qh, D ** -0.5)
+    close(o1, want, ref.attention_tolerance(BF, want, a, smax, D), "attention")
+
+
+def test_attention_two_streams_at_once():
+    """Calls with workspaces of their own may overlap."""
+    cases = [ref.batch([(1, 9000), (1, 4000)], 16, 5, 128, seed=20),
+             ref.batch([(300, 900)], 16, 5, 128, seed=21)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    work = []
+    for s in cases:
+        q = torch.randn(s["M"], 2560, generator=s["g"]).to(BF).cuda()
+        work.append((cuda(s), q, torch.empty_like(q),
+                     bn.alloc_attention_workspace(s["M"], len(s["lens"]), 20, 5, 128)))
+    alone = [run_attention(s, w[1], 20) for s, w in zip(cases, work)]
+    for _ in range(10):
+        for st, (d, q, o, ws) in zip(streams, work):
+            bn.bitnet_attention(q, d["cu"], d["len"], d["table"], d["kc"], d["vc"], o, ws,
+                                stream=st)
+    torch.cuda.synchronize()
+    for want, w in zip(alone, work):
+        assert torch.equal(want, w[2])
+
+
+def test_attention_many_sequences_cut_into_shares():
+    lens = [(1, 1 + (i * 911) % 2500) for i in range(300)] + [(1, 30000)]
+    check_attention(lens, 4, 1, 64, 32, BF)
+
+
 def test_attention_many_sequences():
     lens = [(1 if i % 3 else 0, 1 + (i * 37) % 150) for i in range(400)]
     check_attention(lens, 4, 2, 64, 16, BF)

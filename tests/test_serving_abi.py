@@ -88,6 +88,11 @@ def test_attention_rejects_bad_arguments(kw, code):
     assert attend(**kw) == code
 
 
+def test_attention_refuses_the_queries_buffer_as_output():
+    assert attend(out=FAKE) == INVALID
+    assert "buffer" in bn.bitnet_last_error()
+
+
 def test_attention_workspace_serves_smaller_calls():
     size = bn.bitnet_attention_workspace_size
     for qh, kvh, D in ((20, 5, 128), (8, 8, 64), (4, 2, 256), (20, 1, 96)):
