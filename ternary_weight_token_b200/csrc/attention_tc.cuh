@@ -14,6 +14,13 @@
 // than 2^8 (log2 units); until then the old reference stays, probabilities are
 // at most 2^8 and every sum is unchanged in exact arithmetic.
 //
+// Bound by the alternation of softmax and tensor core: a 4096-token prompt of
+// the 2B heads takes 100 us (855 TFLOP/s, tensor pipe active 42 % of the time).
+// A tile's turn is ~1950 cycles for 1024 of products; what it waits for most
+// is the end of the product with V, before the scores may overwrite the
+// probabilities that product reads (the architecture orders the two only by
+// completion).
+//
 // Warp roles (384 threads, one CTA per SM):
 //   warps 0-3, 4-7  softmax of tile 0, 1: a thread owns a row (TMEM lane)
 //   warp 8          TMA producer: a ring of 128-key slots, K and V in turn,

@@ -18,7 +18,8 @@
 // its heads where tokens are few: it looks the token up and forms its cosines
 // and sines by itself, so warps never wait for one another, and a lane keeps
 // the few angles of its place in the head in registers for all heads.  The
-// first heads are loaded before the token is looked up.
+// first head is loaded before the token is looked up.  Measured: 14.7 us for
+// 3909 tokens (60 MB, 4.1 TB/s), 2.8 us for one.
 #pragma once
 
 #include "common.cuh"
@@ -38,7 +39,9 @@ struct PagedBatch {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 256;
-constexpr int kRopeDepth = 1;          // heads a lane group has in flight
+// Heads a lane group has in flight: with two or four the registers cost more
+// warps than the loads gain (14.7 -> 17.4 / 19 us for 3909 tokens).
+constexpr int kRopeDepth = 1;
 
 struct RopeParams {
   PagedBatch pb;
