@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
   make_plan(p, plan);
 
   uint32_t slot_it = 0;                          // ring position (producer, issuers, warp 10)
+  uint32_t issued = 0;                           // slots whose loads are in flight or done
   uint32_t items_done = 0, fixes = 0, both_done = 0;
   uint32_t blocks_done[2] = {0, 0};              // blocks of tile T so far
 
@@ -346,10 +347,10 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       bool ok = true;
 #pragma unroll 1
       for (int i = 0; i < job.cnt[t]; ++i) {
-        if (!mbar_wait(&sfull[t], (blocks_done[t] + i) & 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
+        // (all lanes agree: what follows is executed by whole warps)
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&sfull[t], (blocks_done[t] + i) & 1u, abort_flag));
+        if (!ok) break;
         tc_fence_after();
         uint32_t s[4][32];
 #pragma unroll
@@ -438,7 +439,8 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       unpack_f32x2(l2, l, lb);
       l += lb;
       if (ok && job.cnt[t] > 0)
-        ok = mbar_wait(&odone[t], (blocks_done[t] + job.cnt[t] - 1) & 1u, abort_flag);
+        ok = __all_sync(0xffffffffu, mbar_wait(&odone[t], (blocks_done[t] + job.cnt[t] - 1) & 1u,
+                                               abort_flag));
       tc_fence_after();
       if (ok && 128 * t < job.q.nrows) {
         float* part = job.q.slot >= 0 ? p.part + (long long)job.q.slot * C::RT * (D + 2) : nullptr;
@@ -543,6 +545,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
             tma_load_3d(dst + h * C::SUB, (i & 1) ? &tm_v : &tm_k, &full[st], 64 * h,
                         key % p.pb.page_size, page * p.kvh + job.q.head);
         }
+        issued = it + 1;
       }
       });
     } else if (warp == 9 || warp == 11) {
@@ -687,9 +690,9 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       mbar_wait(bar, 1, nullptr, 100000000ull);
     }
     if (warp == 8 && lane == 0) {
-      const uint32_t last = slot_it < (uint32_t)C::SLOTS ? slot_it : (uint32_t)C::SLOTS;
+      const uint32_t last = issued < (uint32_t)C::SLOTS ? issued : (uint32_t)C::SLOTS;
       for (uint32_t i = 0; i < last; ++i) {
-        const uint32_t j = slot_it - 1 - i;
+        const uint32_t j = issued - 1 - i;
         mbar_wait(&full[j % C::SLOTS], (j / C::SLOTS) & 1u, nullptr, 100000000ull);
       }
     }

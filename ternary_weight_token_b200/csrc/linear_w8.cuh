@@ -58,7 +58,7 @@ struct W8Config {
   static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
   static constexpr int OFF_X = STAGES * W_STAGE;
   static constexpr int OFF_BAR = OFF_X + STAGES * X_STAGE;
-  static constexpr int NUM_BARS = 2 * STAGES + 5;
+  static constexpr int NUM_BARS = 2 * STAGES + 7;
   static constexpr int OFF_TOK = OFF_BAR + ((NUM_BARS * 8 + 16 + 127) & ~127);  // [2][BN] fp32
   static constexpr int SMEM_ALLOC = OFF_TOK + 2 * BN * 4 + 1024;
   static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "tensor memory");
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint64_t* accfull = bars + 2 * C::STAGES;
   uint64_t* accempty = accfull + 2;
   uint64_t* drain = accempty + 2;
+  uint64_t* tokbar = drain + 1;                  // a tile's token factors are written
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_tok = reinterpret_cast<float*>(smem + C::OFF_TOK);
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
       mbar_init(&accempty[b], 4 * C::GROUPS);
+      mbar_init(&tokbar[b], 4 * C::GROUPS);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -217,12 +219,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int m0 = tm * C::BN;
       const int n = tn * C::BM + 32 * q + lane;
       const bool n_ok = n < p.N;
-      float* tok = s_tok + ab * C::BN;           // read last two tiles ago
+      // this buffer was last read two tiles ago, before its readers arrived for
+      // the tile between
+      float* tok = s_tok + ab * C::BN;
       for (int j = et; j < C::BN; j += 128 * C::GROUPS)
         tok[j] = m0 + j < p.M ? __fdiv_rn(1.0f, p.xs[m0 + j]) : 0.0f;
       const float wf = n_ok ? __fdiv_rn(1.0f, p.ws[n]) : 0.0f;
-      named_bar_sync(1, 128 * C::GROUPS);
-      if (!mbar_wait(&accfull[ab], aph, abort_flag)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tokbar[ab]);
+      const bool ok = mbar_wait(&tokbar[ab], aph, abort_flag) &&
+                      mbar_wait(&accfull[ab], aph, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       constexpr int CW = 16;                      // tokens per step
 #pragma unroll 1
