@@ -765,10 +765,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
 
 // --------------------------------------------------------------- the join
 // CTA (c, y) joins the item that starts in share c and goes on past its end, if
-// there is one: rows y, y + gridDim.y, ... of it (WIDE: four warps take a row
-// each; else they take one row's parts in turn).  The first part is in slot
-// 2 c + 1, those of the shares after it in slots 2 (c + 1), 2 (c + 2), ...
-// Lanes hold 8 values each.
+// there is one.  Its rows are dealt out to the CTAs of c: WIDE, to their warps,
+// as many at a time as fit a warp's lanes; else a row to a CTA, whose warps
+// take the row's parts in turn.  The first part is in slot 2 c + 1, those of
+// the shares after it in slots 2 (c + 1), 2 (c + 2), ...  Lanes hold 8 values
+// each.
 template <bool F32, bool WIDE>
 __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
   __shared__ float s_o[4][kRopeMaxDim];
@@ -808,8 +809,12 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
   const long long size = (long long)RT * (p.D + 2);
   const float* part0 = p.part + (2ll * c + 1) * size;
   const float* part1 = p.part + (2ll * c + 2) * size;        // further parts: 2 size apart
-  for (int rt = WIDE ? blockIdx.y * 4 + warp : blockIdx.y; rt < q.nrows;
-       rt += WIDE ? gridDim.y * 4 : gridDim.y) {
+  const int sub = WIDE ? lane / per : 0, at_once = WIDE ? 32 / per : 1;   // rows of a warp
+  const int ln = WIDE ? lane - sub * per : lane;     // place in the row
+  const int step = WIDE ? gridDim.y * 4 * at_once : gridDim.y;
+  for (int r0 = WIDE ? (blockIdx.y * 4 + warp) * at_once : blockIdx.y; r0 < q.nrows; r0 += step) {
+    const int rt = min(r0 + sub, q.nrows - 1);
+    const bool mine = WIDE ? sub < at_once && r0 + sub < q.nrows : lane < per;
     // one pass with a running maximum: a part's statistics and sums are loaded
     // together, several parts in flight
     float m = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -818,8 +823,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
       const float* f = s == 0 ? part0 : part1 + 2 * (s - 1) * size;
       const float ms = f[rt], ls = f[RT + rt];
       float4 x = make_float4(0, 0, 0, 0), y = x;
-      if (lane < per) {
-        const float4* v = reinterpret_cast<const float4*>(f + 2 * RT + rt * p.D + 8 * lane);
+      if (mine) {
+        const float4* v = reinterpret_cast<const float4*>(f + 2 * RT + rt * p.D + 8 * ln);
         x = v[0];
         y = v[1];
       }
@@ -839,11 +844,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) o[k] *= inv;
-      if (lane < per) {
+      if (mine) {
         if constexpr (F32)
-          store_f32<8>(reinterpret_cast<float*>(p.O) + off + 8 * lane, o);
+          store_f32<8>(reinterpret_cast<float*>(p.O) + off + 8 * ln, o);
         else
-          store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(p.O) + off + 8 * lane, o);
+          store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(p.O) + off + 8 * ln, o);
       }
     } else {
       if (lane == 0) {

@@ -1673,7 +1673,7 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
     rc = f32 ? launch_attn_dim<4, true>(p, di.sms, st) : launch_attn_dim<4, false>(p, di.sms, st);
   if (rc || p.target == 0) return rc;
   // a CTA per share, and per row of its item (16 rows at most, or that many
-  // per sequence on average), or per 32 rows of a wide tile
+  // per sequence on average), or per 16 rows of a wide tile
   if (sh.rt_shift <= 4) {
     const long long rows = ((long long)M * p.G + batch - 1) / batch;
     return launch_pdl(f32 ? attn_join_kernel<true, false> : attn_join_kernel<false, false>,
@@ -1681,7 +1681,7 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
                       dim3(kAttnThreads), 0, st, p);
   }
   return launch_pdl(f32 ? attn_join_kernel<true, true> : attn_join_kernel<false, true>,
-                    dim3((unsigned)p.target, (1u << sh.rt_shift) / 32), dim3(kAttnThreads), 0, st,
+                    dim3((unsigned)p.target, (1u << sh.rt_shift) / 16), dim3(kAttnThreads), 0, st,
                     p);
 }
 
