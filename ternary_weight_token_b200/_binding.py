@@ -257,32 +257,47 @@ def alloc_block_tail_workspace(M, H, I, device="cuda"):
 # pointers).  They run once per layer and token, so the checks are written to
 # cost little: plain tests, messages formed only on failure.
 
-def _device_ptrs(names, tensors):
-    """Addresses of contiguous tensors (None for None), all on the current CUDA device, where
-    the launch goes."""
+_get_device, _is_contiguous, _data_ptr = (torch.Tensor.get_device, torch.Tensor.is_contiguous,
+                                           torch.Tensor.data_ptr)
+_CACHE_TYPES = (torch.bfloat16, torch.bfloat16, torch.int32, torch.int32, torch.int32)
+
+
+def _current_device():
     try:
-        index = torch.cuda.current_device()
-    except (AssertionError, RuntimeError):
-        index = -2
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-        elif t.get_device() == index and t.is_contiguous():
-            out.append(t.data_ptr())
-        else:
-            name = names.split()[len(out)]
-            if not t.is_cuda:
-                raise ValueError(f"{name} must live on a CUDA device")
-            if t.get_device() != index:
-                raise ValueError(f"{name} is on {t.device}, not on the current device")
+        return torch.cuda.current_device()
+    except (AssertionError, RuntimeError):           # no CUDA device
+        return -2
+
+
+def _device_ptrs(names, index, *tensors):
+    """Addresses of contiguous tensors, all on CUDA device `index`, where the launch goes."""
+    if set(map(_get_device, tensors)) == {index} and all(map(_is_contiguous, tensors)):
+        return map(_data_ptr, tensors)
+    for name, t in zip(names.split(), tensors):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must live on a CUDA device")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, not on the current device")
+        if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    return out
 
 
-def _row_stride(name, t, M, width, dtype, device):
+def _optional_ptr(name, index, t):
+    if t is None:
+        return None
+    ptr, = _device_ptrs(name, index, t)
+    return ptr
+
+
+def _stream_on(stream, index):
+    if stream is None and _RAW_STREAM is not None:
+        return _RAW_STREAM(index)
+    return _stream(stream)
+
+
+def _row_stride(name, t, M, width, dtype, index):
     """Row stride of an [M][width] matrix whose rows are contiguous."""
-    if t.shape != (M, width) or t.dtype != dtype or t.get_device() != device:
+    if t.shape != (M, width) or t.dtype != dtype or t.get_device() != index:
         raise ValueError(f"{name} must be [{M}][{width}] of {dtype}, on Q_out's device")
     row, col = t.stride()
     if col != 1:
@@ -292,46 +307,47 @@ def _row_stride(name, t, M, width, dtype, device):
 
 def _paged(cu_q, kv_len, block_table, k_cache, v_cache):
     """(batch, table_stride, num_pages, kv_heads, page_size, head_dim) of a paged cache."""
-    if not (k_cache.dim() == 4 and k_cache.shape == v_cache.shape and
-            k_cache.dtype == torch.bfloat16 and v_cache.dtype == torch.bfloat16):
-        raise ValueError("k_cache and v_cache must be bf16 "
-                         "[num_pages][kv_heads][page_size][head_dim]")
-    if not kv_len.dtype == cu_q.dtype == block_table.dtype == torch.int32:
-        raise ValueError("cu_q, kv_len and block_table must be int32")
-    batch = kv_len.numel()
-    if not (kv_len.dim() == 1 and cu_q.dim() == 1 and cu_q.numel() == batch + 1 and
-            block_table.dim() == 2 and block_table.shape[0] == batch):
-        raise ValueError("kv_len must be [batch], cu_q [batch + 1], "
-                         "block_table [batch][table_stride]")
-    pages, heads, page, dim = k_cache.shape
-    return batch, block_table.shape[1], pages, heads, page, dim
+    shape = k_cache.shape
+    try:
+        pages, heads, page, dim = shape
+        (batch,), (rows, stride), (bounds,) = kv_len.shape, block_table.shape, cu_q.shape
+    except ValueError:
+        batch = rows = bounds = -1
+    if (v_cache.shape != shape or rows != batch or bounds != batch + 1 or
+            (k_cache.dtype, v_cache.dtype, kv_len.dtype, cu_q.dtype, block_table.dtype) !=
+            _CACHE_TYPES):
+        raise ValueError("k_cache and v_cache must be bf16 [num_pages][kv_heads][page_size]"
+                         "[head_dim], cu_q [batch + 1], kv_len [batch] and block_table "
+                         "[batch][table_stride] int32")
+    return batch, stride, pages, heads, page, dim
 
 
 def bitnet_linear_w8(Xq, x_scale, Wq, w_scale, Y, silu=False, residual=None, epilogue=None,
                      stream=None):
     """Y [M][N] = (Xq . Wq^T) / (x_scale[m] w_scale[n]) (int32 Y: the sum itself), the codes
     and scales of both sides from bitnet_quant_act (see include/bitnet.h)."""
-    xq, xs, wq, ws, y, res = _device_ptrs("Xq x_scale Wq w_scale Y residual",
-                                          (Xq, x_scale, Wq, w_scale, Y, residual))
-    if not (Xq.dim() == 2 and Wq.dim() == 2 and Xq.dtype == Wq.dtype == torch.int8 and
-            Xq.shape[1] == Wq.shape[1]):
+    index = _current_device()
+    xq, xs, wq, ws, y = _device_ptrs("Xq x_scale Wq w_scale Y", index, Xq, x_scale, Wq, w_scale, Y)
+    if not (Xq.dim() == 2 and Wq.dim() == 2 and Xq.dtype == Wq.dtype == torch.int8):
         raise ValueError("Xq and Wq must be int8 [M][K] and [N][K]")
-    (M, K), N = Xq.shape, Wq.shape[0]
-    if not (x_scale.dtype == w_scale.dtype == torch.float32 and x_scale.numel() == M and
-            w_scale.numel() == N):
-        raise ValueError("x_scale and w_scale must be fp32 [M] and [N]")
-    if Y.shape != (M, N):
-        raise ValueError("Y must be [M][N]")
-    if residual is not None and not (residual.shape == Y.shape and residual.dtype == Y.dtype):
-        raise ValueError("residual must have Y's shape and type")
+    (M, K), (N, KW) = Xq.shape, Wq.shape
+    if not (K == KW and x_scale.dtype == w_scale.dtype == torch.float32 and
+            x_scale.numel() == M and w_scale.numel() == N and Y.shape == (M, N)):
+        raise ValueError("Xq [M][K] needs Wq [N][K], fp32 x_scale [M] and w_scale [N], Y [M][N]")
     kind = _dtype(Y)
-    if epilogue is None:
-        epilogue = (kind | (BITNET_EPI_SILU if silu else 0) |
-                    (BITNET_EPI_RESIDUAL if residual is not None else 0))
-    elif (epilogue & BITNET_EPI_TYPE_MASK) != kind:
-        raise ValueError("epilogue names another type than Y's")
-    _check(library().bitnet_linear_w8(xq, xs, wq, ws, M, N, K, y, epilogue, res,
-                                      _stream(stream)))
+    flags = kind | BITNET_EPI_SILU if silu else kind
+    res = None
+    if residual is not None:
+        res = _optional_ptr("residual", index, residual)
+        if residual.shape != Y.shape or residual.dtype != Y.dtype:
+            raise ValueError("residual must have Y's shape and type")
+        flags |= BITNET_EPI_RESIDUAL
+    if epilogue is not None:
+        flags = epilogue
+        if (epilogue & BITNET_EPI_TYPE_MASK) != kind:
+            raise ValueError("epilogue names another type than Y's")
+    _check(library().bitnet_linear_w8(xq, xs, wq, ws, M, N, K, y, flags, res,
+                                      _stream_on(stream, index)))
 
 
 def bitnet_rope_append(Q, K, V, inv_freq, cu_q, kv_len, block_table, k_cache, v_cache, Q_out,
@@ -340,25 +356,28 @@ def bitnet_rope_append(Q, K, V, inv_freq, cu_q, kv_len, block_table, k_cache, v_
     """Rotate the new tokens' queries (into Q_out) and keys and append keys and values to the
     paged cache (see include/bitnet.h).  Q, K, V are [M][heads * head_dim]; their rows may be
     strided (slices of one fused projection)."""
-    inv, cu, length, table, kc, vc, out, qg, kg = _device_ptrs(
-        "inv_freq cu_q kv_len block_table k_cache v_cache Q_out q_gain k_gain",
-        (inv_freq, cu_q, kv_len, block_table, k_cache, v_cache, Q_out, q_gain, k_gain))
+    index = _current_device()
+    inv, cu, length, table, kc, vc, out = _device_ptrs(
+        "inv_freq cu_q kv_len block_table k_cache v_cache Q_out", index,
+        inv_freq, cu_q, kv_len, block_table, k_cache, v_cache, Q_out)
     batch, stride, pages, heads, page, dim = _paged(cu_q, kv_len, block_table, k_cache, v_cache)
     if Q_out.dim() != 2 or Q_out.shape[1] % dim:
         raise ValueError("Q_out must be [M][q_heads * head_dim]")
-    (M, width), dtype, device = Q_out.shape, Q_out.dtype, Q_out.get_device()
-    ldq = _row_stride("Q", Q, M, width, dtype, device)
-    ldk = _row_stride("K", K, M, heads * dim, dtype, device)
-    ldv = _row_stride("V", V, M, heads * dim, dtype, device)
+    (M, width), dtype = Q_out.shape, Q_out.dtype
+    ldq = _row_stride("Q", Q, M, width, dtype, index)
+    ldk = _row_stride("K", K, M, heads * dim, dtype, index)
+    ldv = _row_stride("V", V, M, heads * dim, dtype, index)
     if inv_freq.dtype != torch.float32:
         raise ValueError("inv_freq must be fp32")
+    qg, kg = _optional_ptr("q_gain", index, q_gain), _optional_ptr("k_gain", index, k_gain)
     for g in (q_gain, k_gain):
         if g is not None and (g.dtype != torch.float32 or g.numel() != dim):
             raise ValueError("gains must be fp32 [head_dim]")
     _check(library().bitnet_rope_append(
-        Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv, _dtype(Q_out), M, width // dim,
+        _data_ptr(Q), ldq, _data_ptr(K), ldk, _data_ptr(V), ldv, _dtype(Q_out), M, width // dim,
         heads, dim, inv, 2 * inv_freq.numel(), rope | (BITNET_ROPE_HEAD_NORM if head_norm else 0),
-        qg, kg, eps, batch, cu, length, table, stride, kc, vc, pages, page, out, _stream(stream)))
+        qg, kg, eps, batch, cu, length, table, stride, kc, vc, pages, page, out,
+        _stream_on(stream, index)))
 
 
 def bitnet_attention_workspace_size(M, batch, q_heads, kv_heads, head_dim):
@@ -377,9 +396,10 @@ def bitnet_attention(Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspac
                      stream=None):
     """Causal attention of the new tokens over the paged cache (see include/bitnet.h); scale is
     1 / sqrt(head_dim) unless given."""
+    index = _current_device()
     q, cu, length, table, kc, vc, out, ws = _device_ptrs(
-        "Q cu_q kv_len block_table k_cache v_cache O workspace",
-        (Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspace))
+        "Q cu_q kv_len block_table k_cache v_cache O workspace", index,
+        Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspace)
     batch, stride, pages, heads, page, dim = _paged(cu_q, kv_len, block_table, k_cache, v_cache)
     if Q.dim() != 2 or Q.shape[1] % dim:
         raise ValueError("Q must be [M][q_heads * head_dim]")
@@ -389,7 +409,7 @@ def bitnet_attention(Q, cu_q, kv_len, block_table, k_cache, v_cache, O, workspac
     _check(library().bitnet_attention(
         q, _dtype(Q), M, width // dim, heads, dim, dim ** -0.5 if scale is None else scale, batch,
         cu, length, table, stride, kc, vc, pages, page, out, ws, workspace.nbytes,
-        _stream(stream)))
+        _stream_on(stream, index)))
 
 
 BITNET_FFN_NOALLOC_SCRATCH_BYTES = 8 << 20

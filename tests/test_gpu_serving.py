@@ -379,6 +379,42 @@ def test_rope_append_reports_pages_out_of_range():
     assert bn.bitnet_check_device_error() == bn.BITNET_OK
 
 
+def test_binding_refuses_wrong_tensors():
+    """Types, shapes, layouts and devices are checked before anything is launched."""
+    s = ref.batch([(2, 20), (1, 9)], 16, 2, 64, seed=1)
+    d = cuda(s)
+    q, k, v, o = (torch.zeros(3, h * 64, dtype=BF, device="cuda") for h in (8, 2, 2, 8))
+    inv = torch.rand(32, device="cuda")
+    ws = bn.alloc_attention_workspace(3, 2, 8, 2, 64)
+    good = dict(Q=q, cu_q=d["cu"], kv_len=d["len"], block_table=d["table"], k_cache=d["kc"],
+                v_cache=d["vc"], O=o, workspace=ws)
+    bn.bitnet_attention(**good)
+    bad = dict(Q=q[:, :500], cu_q=d["cu"].long(), kv_len=d["len"].float(), O=o.float(),
+               block_table=d["table"][:1], k_cache=d["kc"][:, :, :, :32], workspace=ws.cpu(),
+               v_cache=d["vc"][:2])
+    for key, t in list(bad.items()) + [("cu_q", d["cu"][:2]), ("kv_len", d["len"].cpu()),
+                                       ("Q", q.t().contiguous().t()), ("k_cache", d["kc"][0]),
+                                       ("block_table", d["table"].t().contiguous().t())]:
+        with pytest.raises(ValueError):
+            bn.bitnet_attention(**{**good, key: t})
+    good = dict(Q=q, K=k, V=v, inv_freq=inv, cu_q=d["cu"], kv_len=d["len"],
+                block_table=d["table"], k_cache=d["kc"], v_cache=d["vc"], Q_out=o)
+    for key, t in (("K", k.float()), ("K", q), ("V", v[:2]), ("Q", q.cpu()), ("Q_out", o[:, :64]),
+                   ("inv_freq", inv.double()), ("q_gain", inv), ("k_gain", torch.ones(64)),
+                   ("V", v.t().contiguous().t()), ("Q", q[:, None])):
+        with pytest.raises(ValueError):
+            bn.bitnet_rope_append(**{**good, key: t}, head_norm=True)
+    xq, xs, wq, wsc, _ = (t.cuda() if isinstance(t, torch.Tensor) else t for t in codes(3, 5, 32, 0))
+    y = torch.zeros(3, 5, device="cuda")
+    good = dict(Xq=xq, x_scale=xs, Wq=wq, w_scale=wsc, Y=y)
+    for key, t in (("Xq", xq.float()), ("Wq", wq[:, :16]), ("x_scale", xs[:2]), ("Y", y.t()),
+                   ("w_scale", wsc.double()), ("Y", y.half()), ("residual", y.to(BF)),
+                   ("residual", y.cpu()), ("epilogue", bn.BITNET_BF16), ("Wq", wq[0])):
+        with pytest.raises(ValueError):
+            bn.bitnet_linear_w8(**{**good, key: t})
+    assert bn.bitnet_check_device_error() == bn.BITNET_OK
+
+
 # ------------------------------------------------------------------ int8 product
 
 W8 = [(1, 1, 16), (1, 128, 128), (3, 130, 144), (16, 257, 2560), (17, 64, 272), (33, 1000, 64),
