@@ -16,14 +16,18 @@
 // t * G + g of a sequence is token t, head g of the group, so a tile reads
 // its keys and values once for all of them.
 //
-// Work: a tile of rows (RT) times one key/value head is an item, its blocks of
-// keys (and one more for its start and end) its length in units.  Where the
-// items are too few to deal out evenly, all units of the call are laid end to
-// end and cut into one equal share per CTA, on the device, from the lengths it
-// finds there (so a captured graph keeps fitting as the cache grows).  A CTA
-// whose share starts or ends inside an item writes unnormalised sums and
-// statistics to the workspace and the join kernel adds them; an item inside
-// one share is written directly.
+// Work: a tile of rows (RT) times one key/value head is an item.  Its length is
+// its keys (a linear count, so that items before it add up in closed form) and
+// one block more for its start and end.  Where the items are too few to deal
+// out evenly, all lengths of the call are laid end to end and cut into one
+// equal share per CTA, on the device, from what it finds there (so a captured
+// graph keeps fitting as the cache grows).  A CTA whose share starts or ends
+// inside an item writes unnormalised sums and statistics to the workspace and
+// the join kernel adds them; an item inside one share is written directly.  A
+// call too small to fill the GPU with shares of the smallest size takes those,
+// each item rounded up to whole shares so that no CTA has parts of two.  Where
+// the longest item is little longer than an equal share (`slack`: what cutting
+// and joining cost), items are dealt out whole, longest first.
 #pragma once
 
 #include "common.cuh"
@@ -44,20 +48,35 @@ struct AttnParams {
   int qh, kvh, G, D;
   float scale_log2;                    // softmax scale * log2(e)
   int rt_shift, unit_shift;            // log2 of the rows per tile and the keys per block
-  int min_units;                       // smallest share
+  int min_keys;                        // smallest share, whole blocks
   int target;                          // shares wanted, 0: whole items, dealt out in turn
-  long long* plan;                     // units per share, alignment, units of the call;
-                                       // then the units before each sequence
+  int slack;                           // keys that a whole item may exceed a share by, or -1
+  long long* plan;                     // length of a share, alignment, length of the call;
+                                       // then the lengths before each sequence
   float* part;                         // slots: m[RT], l[RT], o[RT][D]
 };
 
 // --------------------------------------------------------------- the plan
+// Items of a sequence come late tiles first, all heads of a tile together: the
+// items of turn j (tile tiles - 1 - j) are base + slope * (tiles - j) long.
 struct SeqWork {
   int c0, n, len;                      // first row, new tokens, cached tokens
-  int tiles, units;                    // row tiles; units of one item
+  int tiles, base, slope;
 };
 
-// align > 0: items are rounded up to whole shares of that many units.
+__device__ __forceinline__ int item_length(const SeqWork& w, int j) {
+  return w.base + w.slope * (w.tiles - j);
+}
+
+// Length of the sequence's items before turn j.
+__device__ __forceinline__ long long turn_start(const AttnParams& p, const SeqWork& w, int j) {
+  const long long n = j;
+  return p.kvh * (n * w.base + w.slope * (n * w.tiles - n * (n - 1) / 2));
+}
+
+// align > 0: items are rounded up to whole shares of that length; kWhole: every
+// item counts one.
+constexpr int kWhole = -1;
 __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool report, int align) {
   SeqWork w;
   w.c0 = __ldg(p.pb.cu_q + b);
@@ -76,21 +95,25 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool rep
     w.len = w.len < 0 ? 0 : cap;
   }
   w.tiles = (w.n * p.G + (1 << p.rt_shift) - 1) >> p.rt_shift;
-  w.units = 1;
-  if (p.target > 0) {
-    const int blocks = (w.len + (1 << p.unit_shift) - 1) >> p.unit_shift;
-    w.units = align > 0 ? max((blocks + align - 1) / align, 1) * align : blocks + 1;
+  w.slope = 0;
+  if (align == kWhole) {
+    w.base = 1;
+  } else if (align > 0) {
+    w.base = max((w.len + align - 1) / align, 1) * align;
+  } else {
+    w.base = max(w.len - w.n, 0) + (1 << p.unit_shift);
+    w.slope = (1 << p.rt_shift) / p.G;               // tokens of a tile
   }
   return w;
 }
 
 // Thread t of the CTA holds sequences [t per, (t + 1) per) of the batch.
 struct PlanShared {
-  long long share, total;              // units per share, of the call
-  int align;                           // items are whole shares of that many units, or 0
+  long long share, total;              // length of a share, of the call
+  int align;                           // items are whole shares of that length, 0, or kWhole
   long long cursor;                    // where this CTA's share goes on
-  long long first[kAttnThreads + 1];   // units before each thread's sequences
-  long long red[kAttnThreads / 32];
+  long long first[kAttnThreads + 1];   // lengths before each thread's sequences
+  long long red[kAttnThreads / 32], sums[kAttnThreads / 32][3];
 };
 
 // All threads of the CTA, kAttnThreads at least (sequences of later threads
@@ -100,14 +123,45 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
   const int per = (B + kAttnThreads - 1) / kAttnThreads;
   const int b0 = tid * per, b1 = min(B, b0 + per);
   const bool first = blockIdx.x == 0;
+  bool cut = p.target > 0;
+  if (cut && p.slack >= 0) {
+    // length and items of the call, and the longest item
+    long long v[3] = {0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+      const SeqWork w = seq_work(p, b, false, 0);
+      v[0] += turn_start(p, w, w.tiles);
+      v[1] += (long long)w.tiles * p.kvh;
+      if (w.tiles > 0) v[2] = max(v[2], (long long)item_length(w, 0));
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      for (int o = 16; o > 0; o /= 2) {
+        const long long x = __shfl_xor_sync(0xffffffffu, v[k], o);
+        v[k] = k == 2 ? max(v[k], x) : v[k] + x;
+      }
+      if (lane == 0 && warp < kAttnThreads / 32) s.sums[warp][k] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      v[k] = 0;
+      for (int i = 0; i < kAttnThreads / 32; ++i)
+        v[k] = k == 2 ? max(v[k], s.sums[i][k]) : v[k] + s.sums[i][k];
+    }
+    // dealt out whole: the longest item, or the average load and half an item
+    // where the CTAs do not come out even
+    const long long equal = (v[0] + p.target - 1) / p.target;
+    const long long whole = max(v[2], equal + (v[1] > p.target ? v[0] / v[1] / 2 : 0));
+    cut = whole > equal + p.slack;
+  }
   // smallest shares first; if those are too many, equal ones
-  int align = p.target > 0 ? p.min_units : 0;
-  long long share = max(align, 1), mine, sum, total;
+  int align = cut ? p.min_keys : kWhole;
+  long long share = cut ? align : 1, mine, sum, total;
   for (;;) {
     mine = 0;
     for (int b = b0; b < b1; ++b) {
       const SeqWork w = seq_work(p, b, first, align);
-      mine += (long long)w.tiles * p.kvh * w.units;
+      mine += turn_start(p, w, w.tiles);
     }
     sum = mine;                        // inclusive scan
     for (int o = 1; o < 32; o *= 2) {
@@ -119,11 +173,11 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
     for (int i = 0; i < warp && i < kAttnThreads / 32; ++i) sum += s.red[i];
     total = 0;
     for (int i = 0; i < kAttnThreads / 32; ++i) total += s.red[i];
-    if (align == 0 || total <= share * p.target) break;
+    if (align <= 0 || total <= share * p.target) break;
     align = 0;
     __syncthreads();
   }
-  if (p.target > 0 && align == 0) share = max((total + p.target - 1) / p.target, 1ll);
+  if (align == 0) share = max((total + p.target - 1) / p.target, 1ll);
   if (tid < kAttnThreads) s.first[tid] = sum - mine;
   if (tid == 0) {
     s.first[kAttnThreads] = total;
@@ -142,7 +196,7 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
     for (int b = b0; b < b1; ++b) {
       const SeqWork w = seq_work(p, b, false, align);
       p.plan[kAttnPlanHead + b] = at;
-      at += (long long)w.tiles * p.kvh * w.units;
+      at += turn_start(p, w, w.tiles);
     }
   }
   __syncthreads();
@@ -158,24 +212,41 @@ struct AttnPiece {
   int blk0, blk1;
 };
 
-// Units x0 .. x1 of item `local` of a sequence.  Late tiles see the most keys,
-// so they come first.
-__device__ __forceinline__ AttnPiece piece_of(const AttnParams& p, int b, const SeqWork& w,
-                                              int local, int x0, int x1, int slot) {
+// The part x0 .. x1 of an item of turn j.
+__device__ __forceinline__ AttnPiece piece_of(const AttnParams& p, int b, const SeqWork& w, int j,
+                                              int head, int x0, int x1, int slot) {
   AttnPiece q;
-  const int up = local / p.kvh;
   q.b = b;
   q.c0 = w.c0;
-  q.head = local - up * p.kvh;
+  q.head = head;
   q.slot = slot;
-  q.row0 = (w.tiles - 1 - up) << p.rt_shift;
+  q.row0 = (w.tiles - 1 - j) << p.rt_shift;
   q.nrows = min(1 << p.rt_shift, w.n * p.G - q.row0);
   q.past = w.len - w.n;
   q.kv_end = max(0, q.past + (q.row0 + q.nrows - 1) / p.G + 1);
   const int blocks = (q.kv_end + (1 << p.unit_shift) - 1) >> p.unit_shift;
-  q.blk0 = x0 == 0 ? 0 : (int)((long long)blocks * x0 / w.units);
-  q.blk1 = x1 == w.units ? blocks : (int)((long long)blocks * x1 / w.units);
+  const int length = item_length(w, j);
+  q.blk0 = x0 == 0 ? 0 : (int)((long long)blocks * x0 / length);
+  q.blk1 = x1 == length ? blocks : (int)((long long)blocks * x1 / length);
   return q;
+}
+
+// Turn and head of the item at `rel` in a sequence, and where it starts there.
+__device__ __forceinline__ long long item_at(const AttnParams& p, const SeqWork& w, long long rel,
+                                             int& j, int& head) {
+  int lo = 0, hi = w.tiles - 1;        // the last turn that starts at rel or before
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (turn_start(p, w, mid) <= rel)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  j = lo;
+  const long long start = turn_start(p, w, j);
+  const int length = item_length(w, j);
+  head = (int)((rel - start) / length);
+  return start + (long long)head * length;
 }
 
 // Whole item c: calls take(piece) on the one thread whose sequences hold it
@@ -191,7 +262,8 @@ __device__ __forceinline__ void find_item(const AttnParams& p, const PlanShared&
     const SeqWork w = seq_work(p, b, false, s.align);
     const long long k = (long long)w.tiles * p.kvh;
     if (c < at + k) {
-      take(piece_of(p, b, w, (int)(c - at), 0, 1, -1));
+      const int local = (int)(c - at), j = local / p.kvh;
+      take(piece_of(p, b, w, j, local - j * p.kvh, 0, item_length(w, j), -1));
       return;
     }
     at += k;
@@ -219,16 +291,24 @@ __device__ __forceinline__ void next_pieces(const AttnParams& p, PlanShared& s, 
   int k = 0;
   for (int b = tid * per; b < p.pb.batch && k < most && pos < end; ++b) {
     const SeqWork w = seq_work(p, b, false, s.align);
-    const long long all = (long long)w.tiles * p.kvh * w.units;
-    while (pos < at + all && k < most && pos < end) {
-      const int local = (int)((pos - at) / w.units);
-      const long long item = at + (long long)local * w.units;
-      const int x0 = (int)(pos - item);
-      const int x1 = (int)min((long long)w.units, end - item);
-      const int slot =
-          x0 == 0 && x1 == w.units ? -1 : 2 * (int)blockIdx.x + (x0 == 0 ? 1 : 0);
-      take(k++, piece_of(p, b, w, local, x0, x1, slot));
-      pos = item + x1;
+    const long long all = turn_start(p, w, w.tiles);
+    if (pos < at + all) {
+      int j, head;
+      long long item = at + item_at(p, w, pos - at, j, head);
+      for (;;) {
+        const int length = item_length(w, j);
+        const int x0 = (int)(pos - item);
+        const int x1 = (int)min((long long)length, end - item);
+        const int slot = x0 == 0 && x1 == length ? -1 : 2 * (int)blockIdx.x + (x0 == 0 ? 1 : 0);
+        take(k++, piece_of(p, b, w, j, head, x0, x1, slot));
+        pos = item + x1;
+        item += length;
+        if (++head == p.kvh) {
+          head = 0;
+          ++j;
+        }
+        if (j == w.tiles || k == most || pos >= end) break;
+      }
     }
     at += all;
   }
@@ -339,7 +419,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
   for (long long c = blockIdx.x;; c += gridDim.x) {
     if (tid == 0) s_count = 0;
     __syncthreads();
-    if (p.target > 0)
+    if (plan.align != kWhole)
       next_pieces(p, plan, 1, s_count, [&](int, const AttnPiece& q) { s_piece = q; });
     else if (c < plan.total)
       find_item(p, plan, c, [&](const AttnPiece& q) {
@@ -348,7 +428,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
       });
     __syncthreads();
     if (s_count == 0) {
-      if (p.target > 0 || c + gridDim.x >= plan.total) break;
+      if (plan.align != kWhole || c + gridDim.x >= plan.total) break;
       __syncthreads();
       continue;
     }
@@ -781,8 +861,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
   const int align = (int)p.plan[1];
   const int c = blockIdx.x;
   const long long end = share * (c + 1);
-  if (end >= total) return;
-  // the sequence that holds unit end - 1: the last one that starts before it
+  if (align == kWhole || end >= total) return;
+  // the sequence that holds place end - 1: the last one that starts before it
   int b = -1;
   for (int base = 0; base < p.pb.batch; base += 128) {
     int in = 0;
@@ -799,11 +879,13 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
   }
   const SeqWork w = seq_work(p, b, false, align);
   const long long at = p.plan[kAttnPlanHead + b];
-  const int local = (int)((end - 1 - at) / w.units);
-  const long long item = at + (long long)local * w.units;
-  if (item + w.units <= end || item < end - share) return;   // does not go on, or began before
-  const int splits = (int)((item + w.units - 1) / share) - c + 1;
-  const AttnPiece q = piece_of(p, b, w, local, 0, w.units, -1);
+  if (w.tiles == 0) return;                          // the lengths changed under the call
+  int j, head;
+  const long long item = at + item_at(p, w, end - 1 - at, j, head);
+  const int length = item_length(w, j);
+  if (item + length <= end || item < end - share) return;    // does not go on, or began before
+  const int splits = (int)((item + length - 1) / share) - c + 1;
+  const AttnPiece q = piece_of(p, b, w, j, head, 0, length, -1);
 
   const int RT = 1 << p.rt_shift, per = p.D / 8;
   const long long size = (long long)RT * (p.D + 2);

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       if (threadIdx.x < kAttnTcList) items[threadIdx.x].count = -1;
       if (threadIdx.x == 0) *listed = 0;
       __syncthreads();
-      if (p.target > 0) {
+      if (plan.align != kWhole) {
         next_pieces(p, plan, kAttnTcList, *listed, lay_out);
       } else {
         for (int k = 0; k < kAttnTcList; ++k) {

@@ -871,7 +871,7 @@ int validate_paged(int dtype, int M, int q_heads, int kv_heads, int head_dim, in
 // Kernel and row tile of an attention call (pure host logic).
 struct AttnShape {
   bool tc;                             // tensor-core kernel
-  int rt_shift, unit_shift, min_units, target;
+  int rt_shift, unit_shift, min_units, target;   // min_units: blocks of the smallest share
 };
 
 AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, bool f32,
@@ -897,8 +897,9 @@ AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, 
     sh.min_units = sh.rt_shift <= 4 ? 2 : 8;
     sh.target = kAttnTarget;
   }
-  // enough items to deal out whole
-  if (((long long)M * G >> sh.rt_shift) * kv_heads >= 2 * sh.target) sh.target = 0;
+  // enough items of chunks to deal out whole, longest first (decode is cut into
+  // equal shares whatever its items: their lengths may differ by any factor)
+  if (sh.rt_shift > 4 && (rows >> sh.rt_shift) * kv_heads >= 2 * sh.target) sh.target = 0;
   return sh;
 }
 
@@ -1655,7 +1656,11 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   p.qh = q_heads; p.kvh = kv_heads; p.G = q_heads / kv_heads; p.D = head_dim;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.rt_shift = sh.rt_shift; p.unit_shift = sh.unit_shift;
-  p.min_units = sh.min_units; p.target = sh.target;
+  p.min_keys = sh.min_units << sh.unit_shift; p.target = sh.target;
+  // cutting and joining cost the tensor-core kernel about as much as ten blocks
+  // (one prompt of 3000 tokens: 77 us whole, 113 cut; four chunks over 1281 - 3782
+  // keys 82.6 / 83.6; two chunks of 1000 over 3000: 95 / 88)
+  p.slack = sh.tc ? 10 * kAttnTcKeys : -1;
   // sequences shorter than the smallest share are not worth cutting
   if ((long long)table_stride * page_size < (long long)sh.min_units << sh.unit_shift) p.target = 0;
   p.plan = reinterpret_cast<long long*>(workspace);
