@@ -100,6 +100,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b, bool rep
     w.base = 1;
   } else if (align > 0) {
     w.base = max((w.len + align - 1) / align, 1) * align;
+  } else if (w.tiles <= 1) {                         // whole blocks, as shares are
+    w.base = (((w.len - 1) >> p.unit_shift) + 2) << p.unit_shift;
   } else {
     w.base = max(w.len - w.n, 0) + (1 << p.unit_shift);
     w.slope = (1 << p.rt_shift) / p.G;               // tokens of a tile
@@ -113,7 +115,7 @@ struct PlanShared {
   int align;                           // items are whole shares of that length, 0, or kWhole
   long long cursor;                    // where this CTA's share goes on
   long long first[kAttnThreads + 1];   // lengths before each thread's sequences
-  long long red[kAttnThreads / 32], sums[kAttnThreads / 32][3];
+  long long red[kAttnThreads / 32], sums[kAttnThreads / 32][4];
 };
 
 // All threads of the CTA, kAttnThreads at least (sequences of later threads
@@ -125,33 +127,43 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
   const bool first = blockIdx.x == 0;
   bool cut = p.target > 0;
   if (cut && p.slack >= 0) {
-    // length and items of the call, and the longest item
-    long long v[3] = {0, 0, 0};
+    // length and items of the call, the longest and the shortest item (negated)
+    long long v[4] = {0, 0, 0, -(1ll << 40)};
     for (int b = b0; b < b1; ++b) {
       const SeqWork w = seq_work(p, b, false, 0);
       v[0] += turn_start(p, w, w.tiles);
       v[1] += (long long)w.tiles * p.kvh;
-      if (w.tiles > 0) v[2] = max(v[2], (long long)item_length(w, 0));
+      if (w.tiles > 0) {
+        v[2] = max(v[2], (long long)item_length(w, 0));
+        v[3] = max(v[3], -(long long)item_length(w, w.tiles - 1));
+      }
     }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < 4; ++k) {
       for (int o = 16; o > 0; o /= 2) {
         const long long x = __shfl_xor_sync(0xffffffffu, v[k], o);
-        v[k] = k == 2 ? max(v[k], x) : v[k] + x;
+        v[k] = k >= 2 ? max(v[k], x) : v[k] + x;
       }
       if (lane == 0 && warp < kAttnThreads / 32) s.sums[warp][k] = v[k];
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      v[k] = 0;
-      for (int i = 0; i < kAttnThreads / 32; ++i)
-        v[k] = k == 2 ? max(v[k], s.sums[i][k]) : v[k] + s.sums[i][k];
+    for (int k = 0; k < 4; ++k) {
+      v[k] = s.sums[0][k];
+      for (int i = 1; i < kAttnThreads / 32; ++i)
+        v[k] = k >= 2 ? max(v[k], s.sums[i][k]) : v[k] + s.sums[i][k];
     }
-    // dealt out whole: the longest item, or the average load and half an item
-    // where the CTAs do not come out even
-    const long long equal = (v[0] + p.target - 1) / p.target;
-    const long long whole = max(v[2], equal + (v[1] > p.target ? v[0] / v[1] / 2 : 0));
+    // Dealt out whole, as many items as CTAs take the longest one's time; up to
+    // twice as many, CTA i takes items i and 2 CTAs - 1 - i, the worst of them
+    // the first that has two (lengths taken to fall evenly); more, half an item
+    // over the average.
+    const long long items = v[1], ctas = p.target, shortest = -v[3];
+    const long long equal = (v[0] + ctas - 1) / ctas;
+    long long whole = max(v[2], equal);
+    if (items > 2 * ctas)
+      whole = max(whole, equal + v[0] / items / 2);
+    else if (items > ctas)
+      whole = max(whole, v[2] - (v[2] - shortest) * (2 * ctas - items) / items + shortest);
     cut = whole > equal + p.slack;
   }
   // smallest shares first; if those are too many, equal ones
@@ -177,7 +189,10 @@ __device__ __forceinline__ void make_plan(const AttnParams& p, PlanShared& s) {
     align = 0;
     __syncthreads();
   }
-  if (align == 0) share = max((total + p.target - 1) / p.target, 1ll);
+  if (align == 0 && p.slack >= 0)
+    share = max((total + p.target - 1) / p.target, 1ll);
+  else if (align == 0)                 // decode: whole blocks, as its items are
+    share = ((((total + p.target - 1) / p.target - 1) >> p.unit_shift) + 1) << p.unit_shift;
   if (tid < kAttnThreads) s.first[tid] = sum - mine;
   if (tid == 0) {
     s.first[kAttnThreads] = total;
@@ -356,8 +371,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ------------------------------------------------------- mma.sync kernel
-// Bound by HBM once sequences are long: 49 us for 32 sequences of 95144 cached
-// tokens (244 MB, 5.0 TB/s with plan and join), 65 us for two of 129198; by
+// Bound by HBM once sequences are long: 50 us for 32 sequences of 95144 cached
+// tokens (244 MB, 4.9 TB/s with plan and join), 65 us for two of 129198; by
 // latency when short: 11 us for one token over 715.
 //
 // Four warps: WR of them along the rows (16 each), 4 / WR along the keys of a

@@ -15,7 +15,7 @@
 // at most 2^8 and every sum is unchanged in exact arithmetic.
 //
 // Bound by the alternation of softmax and tensor core: a 4096-token prompt of
-// the 2B heads takes 100 us (855 TFLOP/s, tensor pipe active 42 % of the time).
+// the 2B heads takes 101 us (850 TFLOP/s, tensor pipe active 42 % of the time).
 // A tile's turn is ~1950 cycles for 1024 of products; what it waits for most
 // is the end of the product with V, before the scores may overwrite the
 // probabilities that product reads (the architecture orders the two only by

@@ -1657,10 +1657,10 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.rt_shift = sh.rt_shift; p.unit_shift = sh.unit_shift;
   p.min_keys = sh.min_units << sh.unit_shift; p.target = sh.target;
-  // cutting and joining cost the tensor-core kernel about as much as ten blocks
-  // (one prompt of 3000 tokens: 77 us whole, 113 cut; four chunks over 1281 - 3782
-  // keys 82.6 / 83.6; two chunks of 1000 over 3000: 95 / 88)
-  p.slack = sh.tc ? 10 * kAttnTcKeys : -1;
+  // cutting and joining cost the tensor-core kernel about as much as twelve
+  // blocks (one prompt of 3000 tokens: 77 us whole, 113 cut; four chunks over
+  // 1281 - 3782 keys 82.6 / 84.8; two chunks of 1000 over 3000: 95 / 88)
+  p.slack = sh.tc ? 12 * kAttnTcKeys : -1;
   // sequences shorter than the smallest share are not worth cutting
   if ((long long)table_stride * page_size < (long long)sh.min_units << sh.unit_shift) p.target = 0;
   p.plan = reinterpret_cast<long long*>(workspace);

@@ -129,6 +129,7 @@ def test_attention_long_history_of_a_chunk(dtype):
     """Few items over many keys: every one is cut into many shares."""
     check_attention([(40, 20011)], 8, 8, 64, 32, dtype)
     check_attention([(9, 6000), (90, 133)], 20, 1, 96, 16, dtype)
+    check_attention([(300, 4000), (2, 2)], 20, 5, 128, 64, dtype)
 
 
 def test_attention_ten_new_tokens_each():
