@@ -32,6 +32,7 @@
 
 #include "attention.cuh"
 #include "common.cuh"
+#include "gemv_tc.cuh"
 
 namespace bitnet {
 

@@ -14,9 +14,7 @@ namespace bitnet {
 // ---------------------------------------------------------------- errors
 // Device error word: kernels OR a code into it when a bounded wait gives up.
 // The host reads and clears it in bitnet_check_device_error().
-// DEV_ERR_INDEX: a page index or a length in device memory is out of range; the
-// kernel skipped the access.
-enum : unsigned { DEV_ERR_TIMEOUT = 1u, DEV_ERR_INDEX = 2u };
+enum : unsigned { DEV_ERR_TIMEOUT = 1u };
 
 __device__ unsigned int g_device_error = 0;
 
@@ -247,17 +245,6 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
         "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
-// 32 lanes x 16 columns.
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 

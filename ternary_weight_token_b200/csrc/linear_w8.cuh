@@ -25,6 +25,7 @@
 
 #include "common.cuh"
 #include "gemv.cuh"
+#include "gemv_tc.cuh"
 
 namespace bitnet {
 

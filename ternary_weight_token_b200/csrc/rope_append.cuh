@@ -26,6 +26,10 @@
 
 namespace bitnet {
 
+// Device error word: a page index, row or length in device memory is out of
+// range; the kernel skipped the access.
+constexpr unsigned DEV_ERR_INDEX = 2u;
+
 // Where the new tokens of a batch of sequences stand, and the pages that hold
 // their past: shared by the append and by the attention that reads the cache.
 struct PagedBatch {
