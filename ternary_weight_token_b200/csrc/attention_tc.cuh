@@ -15,7 +15,7 @@
 // at most 2^8 and every sum is unchanged in exact arithmetic.
 //
 // Bound by the alternation of softmax and tensor core: a 4096-token prompt of
-// the 2B heads takes 101 us (850 TFLOP/s, tensor pipe active 42 % of the time).
+// the 2B heads takes 104 us (822 TFLOP/s, tensor pipe active 42 % of the time).
 // A tile's turn is ~1950 cycles for 1024 of products; what it waits for most
 // is the end of the product with V, before the scores may overwrite the
 // probabilities that product reads (the architecture orders the two only by
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
   uint64_t* sfull = turn + 2;                    // [T] scores ready (commit)
   uint64_t* pfull = sfull + 2;                   // [T][half] probabilities written (4 warps)
   uint64_t* odone = pfull + 4;                   // [T] product with V done (commit)
-  uint64_t* vlast = odone + 2;                   // the block with the last key is here (issuer)
+  uint64_t* vlast = odone + 2;                   // both issuers are at the last key's block
   uint64_t* vfix = vlast + 1;                    // its rows past that key are zeroed (warp 10)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       mbar_init(&pfull[2 * t + 1], 4);
       mbar_init(&odone[t], 1);
     }
-    mbar_init(vlast, 1);
+    mbar_init(vlast, 2);
     mbar_init(vfix, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
 
   uint32_t slot_it = 0;                          // ring position (producer, issuers, warp 10)
   uint32_t issued = 0;                           // slots whose loads are in flight or done
-  uint32_t items_done = 0, fixes = 0, both_done = 0;
+  uint32_t fixes = 0, both_done = 0;
+  uint32_t tiles_done[2] = {0, 0};               // items in which tile T has blocks
   uint32_t blocks_done[2] = {0, 0};              // blocks of tile T so far
 
   // Every role walks the same items, each at its own pace: the barriers above
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         blocks_done[0] += job.cnt[0];
         blocks_done[1] += job.cnt[1];
         both_done += min(job.cnt[0], job.cnt[1]);
-        ++items_done;
+        if (job.cnt[0] > 0) ++tiles_done[0];
+        if (job.cnt[1] > 0) ++tiles_done[1];
         if (job.fix) ++fixes;
         if (*abort_flag) break;
       }
@@ -320,7 +322,9 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
           }
         }
       };
-      {
+      // (without blocks there is nothing to wait for on either side: the softmax
+      // would run ahead of its issuer by more than one phase of the barrier)
+      if (job.cnt[t] > 0) {
         uint4 u[LR];
         each_row([&](int k, long long off) {
           u[k] = make_uint4(0, 0, 0, 0);
@@ -557,9 +561,15 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       // tensor core works for the other (one issuer for both in turn left it
       // idle half of the time).  The whole warp follows the loop and one
       // elected lane issues, so that descriptors live in uniform registers.
-      // Each barrier is waited for in every one of its phases, needed or not: a
-      // parity wait that skips one may take the phase before for its own.
-      bool ok = __all_sync(0xffffffffu, mbar_wait(&qfull[t], items_done & 1u, abort_flag));
+      // A parity wait may take the phase before for its own if one is skipped, and
+      // misses its own if the barrier gets two ahead.  So every waiter waits in
+      // every phase, and no barrier can complete a phase before all its waiters
+      // have seen the last: slots need both issuers' release, vlast both their
+      // arrivals, the others go to and fro between two sides.
+      const int cnt = t == 0 ? job.cnt[0] : job.cnt[1];
+      const uint32_t q_phase = t == 0 ? tiles_done[0] : tiles_done[1];
+      bool ok = true;
+      if (cnt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&qfull[t], q_phase & 1u, abort_flag));
       if (job.count > 0) {
         constexpr uint32_t idesc_s = make_idesc_bf16(128, 128, false);
         constexpr uint32_t idesc_o = make_idesc_bf16(128, DP, true);
@@ -567,10 +577,8 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         const uint32_t kva = smem_u32(smem) + C::OFF_KV;
         const uint64_t qd = make_sdesc_sw128(smem_u32(smem) + t * C::TILE);
         const uint32_t dcol = tbase + C::O_COL + 128u * t, scol = tbase + C::S_COL + 128u * t;
-        const int cnt = t == 0 ? job.cnt[0] : job.cnt[1];
         const uint32_t done0 = t == 0 ? blocks_done[0] : blocks_done[1];
         const int both = min(job.cnt[0], job.cnt[1]);
-        const bool last_here = cnt == job.count && (t == 1 || job.cnt[1] < job.count);
         // pass: hand the turn over half way, since it takes the other issuer
         // about as long as the second half to notice
         auto scores = [&](uint32_t st, bool pass) {
@@ -603,18 +611,22 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
           const bool more = i + 1 < job.count;
           if (i >= cnt) {                        // the other tile sees more keys
             ok = mbar_wait(&full[sv], (it / C::SLOTS) & 1u, abort_flag);
-            if (job.fix && !more) ok = ok && mbar_wait(vfix, fixes & 1u, abort_flag);
+            if (job.fix && !more) {
+              if (ok && leader) mbar_arrive(vlast);
+              ok = ok && mbar_wait(vfix, fixes & 1u, abort_flag);
+            }
+            ok = __all_sync(0xffffffffu, ok);    // every lane has seen the phase
             if (ok && lane == 0) mbar_arrive(&empty[sv]);
-            if (more) {
-              ok = ok && mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag);
+            if (ok && more) {
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait(&full[sk], ((it + 1) / C::SLOTS) & 1u, abort_flag));
               if (ok && lane == 0) mbar_arrive(&empty[sk]);
             }
-            ok = __all_sync(0xffffffffu, ok);
             continue;
           }
           ok = mbar_wait(&full[sv], (it / C::SLOTS) & 1u, abort_flag);
           if (job.fix && !more) {
-            if (ok && leader && last_here) mbar_arrive(vlast);
+            if (ok && leader) mbar_arrive(vlast);
             ok = ok && mbar_wait(vfix, fixes & 1u, abort_flag);
           }
           const uint64_t vd = make_sdesc_mn_sw128(kva + sv * C::TILE, C::SUB);

@@ -132,6 +132,18 @@ def test_attention_long_history_of_a_chunk(dtype):
     check_attention([(300, 4000), (2, 2)], 20, 5, 128, 64, dtype)
 
 
+@pytest.mark.parametrize("case", [
+    ([(1, 1 + i % 9) for i in range(60)] + [(1500, 1500)], 64, 64, 64, 16),
+    ([(300, 4000)] + [(2, 2 + i % 7) for i in range(30)], 20, 5, 128, 64),
+    ([(1, 1 + 3 * i) for i in range(30)] + [(129, 300), (40, 0), (2, 140)], 20, 20, 128, 16),
+    ([(0, 9), (33, 129)] * 40, 4, 4, 128, 32),
+], ids=["decode among a prompt", "short after cut", "odd tiles", "empty between"])
+def test_attention_many_short_items_on_the_tensor_cores(case):
+    """CTAs run through many items in a row that have one row tile or one block."""
+    for _ in range(3):
+        check_attention(*case, BF)
+
+
 def test_attention_ten_new_tokens_each():
     """More than 16 rows a sequence, all in one tile; then 9 to 16 rows."""
     check_attention([(10, 500)] * 7, 20, 5, 128, 16, BF)
