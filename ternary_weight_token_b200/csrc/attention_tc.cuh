@@ -171,13 +171,38 @@ struct AttnTcConfig {
       OFF_ITEMS + kAttnTcList * (int)sizeof(AttnTcItem) + 16 + 1024;            // + alignment slack
   static constexpr uint32_t S_COL = 0, O_COL = 256;          // + 128 T
   static_assert(OFF_PLAN % 16 == 0 && SMEM <= 227 * 1024, "shared memory");
+
+  // Byte offset in a row tile of 16-byte chunk c of row r.  A softmax warp's 32
+  // rows hold its queries, then its outputs or its fp32 sums: the four warps of a
+  // tile go from item to item without a common barrier, so whatever a warp
+  // puts there has to lie in its own rows.
+  __host__ __device__ static constexpr int row_chunk(int r, int c) {
+    return (c >> 3) * SUB + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  }
 };
+
+// Every chunk of a row lies in the 128 bytes that each half of the tile has for
+// that row, and no two coincide.
+template <class C>
+constexpr bool attn_tc_rows_apart() {
+  for (int r = 0; r < 128; ++r) {
+    unsigned seen = 0;
+    for (int c = 0; c < 8 * C::HALVES; ++c) {
+      const int at = C::row_chunk(r, c), half = at / C::SUB, in = at % C::SUB;
+      if (half >= C::HALVES || in / 128 != r || in % 16 != 0) return false;
+      seen |= 1u << (8 * half + in % 128 / 16);
+    }
+    if (seen != (1u << (8 * C::HALVES)) - 1u) return false;
+  }
+  return true;
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kAttnTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, AttnParams p, int box_rows) {
   using C = AttnTcConfig<DP>;
+  static_assert(attn_tc_rows_apart<C>(), "a row's chunks lie in its own bytes");
   extern __shared__ uint8_t attn_tc_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(attn_tc_raw) + 1023) & ~uintptr_t(1023));
@@ -304,7 +329,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       // LR lanes per row, rows sub, sub + 32 / LR, ... of the warp's 32.
       constexpr int LR = DP / 8, STEP = 32 / LR;
       const int ch = lane % LR, sub = lane / LR, wrow = 32 * (warp & 3);
-      uint8_t* qtile = smem + t * C::TILE + (ch >> 3) * C::SUB;
+      uint8_t* qtile = smem + t * C::TILE;
       // element offset of the first such row, and the way to the next
       const int gr0 = job.q.row0 + 128 * t + wrow + sub;
       const int tok0 = gr0 / p.G, g0 = gr0 - tok0 * p.G;
@@ -335,7 +360,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
 #pragma unroll
         for (int k = 0; k < LR; ++k) {
           const int rr = wrow + sub + STEP * k;
-          *reinterpret_cast<uint4*>(qtile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = u[k];
+          *reinterpret_cast<uint4*>(qtile + C::row_chunk(rr, ch)) = u[k];
         }
         fence_proxy_async_shared();
         __syncwarp();
@@ -454,8 +479,9 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
           part[row] = m;
           part[C::RT + row] = l;
         }
-        // The rows leave through the Q tile, which is done with, so that a warp
-        // stores whole rows: W columns at a time, bf16 or fp32 sums.
+        // The rows leave through the warp's own rows of the Q tile, which the
+        // products are done with, so that a warp stores whole rows: bf16, or fp32
+        // sums, as many columns at a time as fit a row's bytes.
         auto columns = [&](int d, float (&x)[8]) {
           uint32_t o[8];
           if (job.cnt[t] > 0) {
@@ -473,22 +499,19 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
           for (int d = 0; d < DP; d += 8) {
             float x[8];
             columns(d, x);
-            store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(
-                              smem + t * C::TILE + (d >> 6) * C::SUB + r * 128 +
-                              (((d >> 3 & 7) ^ (r & 7)) << 4)), x);
+            store_bf16<8>(reinterpret_cast<__nv_bfloat16*>(qtile + C::row_chunk(r, d / 8)), x);
           }
           __syncwarp();
           each_row([&](int k, long long off) {
             const int rr = wrow + sub + STEP * k;
             if (128 * t + rr < job.q.nrows && 8 * ch < D)
               *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.O) + off) =
-                  *reinterpret_cast<const uint4*>(qtile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+                  *reinterpret_cast<const uint4*>(qtile + C::row_chunk(rr, ch));
           });
           __syncwarp();
         } else {
-          constexpr int W = C::TILE / 512, RB = 4 * W;       // columns, bytes of a staged row
-          constexpr int WL = W / 4, WSTEP = 32 / WL;         // lanes per row, rows at a time
-          uint8_t* st = smem + t * C::TILE;
+          // lanes per row: its chunks of four columns; rows at a time
+          constexpr int WL = 8 * C::HALVES, W = 4 * WL, WSTEP = 32 / WL;
 #pragma unroll 1
           for (int d0 = 0; d0 < DP; d0 += W) {
 #pragma unroll 4
@@ -497,7 +520,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
               columns(d0 + d, x);
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float4*>(st + r * RB + (((d / 4 + e) ^ (r & 7)) << 4)) =
+                *reinterpret_cast<float4*>(qtile + C::row_chunk(r, d / 4 + e)) =
                     make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
             __syncwarp();
@@ -506,7 +529,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
             for (int rr = wrow + lane / WL; rr < wrow + 32; rr += WSTEP) {
               if (128 * t + rr < job.q.nrows && d < D)
                 *reinterpret_cast<float4*>(part + 2 * C::RT + (long long)(128 * t + rr) * D + d) =
-                    *reinterpret_cast<const float4*>(st + rr * RB + ((wch ^ (rr & 7)) << 4));
+                    *reinterpret_cast<const float4*>(qtile + C::row_chunk(rr, wch));
             }
             __syncwarp();
           }

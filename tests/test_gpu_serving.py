@@ -144,6 +144,33 @@ def test_attention_many_short_items_on_the_tensor_cores(case):
         check_attention(*case, BF)
 
 
+@pytest.mark.parametrize("case", [
+    ([(300, 9000)], 20, 5, 128, 64),
+    ([(300, 9000), (2, 2), (40, 0), (40, 3000), (130, 5000)], 20, 5, 128, 32),
+    ([(129, 7000), (100, 5500)], 8, 8, 128, 128),
+    ([(33, 20000), (1, 30), (257, 4100)], 6, 2, 128, 16),
+    ([(257, 9001), (64, 64), (500, 6100)], 12, 4, 96, 48),
+], ids=str)
+def test_attention_cut_items_repeat_bit_for_bit(case):
+    """Equal shares: a CTA's part of one item is followed by others without a barrier between its
+    warps, so every run has to give the bits of the first, which is compared with 64 bits."""
+    lens, qh, kvh, D, page = case
+    s = ref.batch(lens, page, kvh, D, seed=31, fill=float("nan"))
+    q = torch.randn(s["M"], qh * D, generator=s["g"]).to(BF)
+    o, a, smax = ref.attention(s, q, qh, D ** -0.5)
+    d, qd = cuda(s), q.cuda()
+    ws = bn.alloc_attention_workspace(s["M"], len(lens), qh, kvh, D)
+    runs = torch.full((60, *q.shape), 7.0, dtype=BF, device="cuda")
+    for out in runs:
+        ws.fill_(0xFF)
+        bn.bitnet_attention(qd, d["cu"], d["len"], d["table"], d["kc"], d["vc"], out, ws)
+    torch.cuda.synchronize()
+    assert bn.bitnet_check_device_error() == bn.BITNET_OK
+    close(runs[0], o, ref.attention_tolerance(BF, o, a, smax, D), "attention")
+    other = [i for i in range(len(runs)) if not torch.equal(runs[i], runs[0])]
+    assert not other, f"runs {other} differ from the first"
+
+
 def test_attention_ten_new_tokens_each():
     """More than 16 rows a sequence, all in one tile; then 9 to 16 rows."""
     check_attention([(10, 500)] * 7, 20, 5, 128, 16, BF)
