@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
         if (job.cnt[0] > 0) ++tiles_done[0];
         if (job.cnt[1] > 0) ++tiles_done[1];
         if (job.fix) ++fixes;
-        if (*abort_flag) break;
+        // another warp may set the flag at any time: the whole warp leaves or stays
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
       }
       if (__syncthreads_or(*abort_flag)) break;
     }
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
   }
 
   // Never leave tensor-core work or bulk copies in flight (an abort can).
-  if (*abort_flag) {
+  if (__any_sync(0xffffffffu, *abort_flag)) {
     if ((warp == 9 || warp == 11) && elect_one()) {
       uint64_t* bar = &odone[warp == 9 ? 0 : 1];
       tc_commit(bar);
