@@ -288,10 +288,11 @@ BITNET_API int bitnet_linear_w8(const int8_t *Xq, const float *x_scale, const in
  * page_size a multiple of 16, table_stride * page_size and M * q_heads at most
  * 2^30.  The
  * tables are device memory read on the stream, so a captured call follows
- * lengths that change between replays.  A page index, row or length out of
- * range is recorded in the device error word (bitnet_check_device_error()
- * returns INVALID_ARG); no access is made there and the outputs of that
- * sequence are unspecified.
+ * lengths that change between replays.  A page index, rows (entries of cu_q
+ * that fall or leave 0 .. M) or a length (negative, or more than table_stride *
+ * page_size) out of range is recorded in the device error word
+ * (bitnet_check_device_error() returns INVALID_ARG); no access is made there
+ * and the outputs of that sequence are unspecified.
  *
  * Rotate the new tokens' queries and keys and append keys and values.
  *   Q, K, V   token rows [M] of q_heads, kv_heads, kv_heads heads of `dtype`

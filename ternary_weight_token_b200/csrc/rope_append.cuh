@@ -61,24 +61,37 @@ struct RopeParams {
   int warps_per_token;              // a power of two up to the CTA's warps
 };
 
-// Sequence of token row r: the number of sequences that end at or before it
+// Sequence of token row r: the first one that ends behind it, or the batch
 // (every lane of the warp gets it).
 __device__ __forceinline__ int sequence_of(const PagedBatch& pb, int r, int lane) {
-  int b = 0;
   for (int base = 0; base < pb.batch; base += 128) {
-    int done[4];
+    bool behind[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = base + 32 * k + lane;
-      done[k] = i < pb.batch && __ldg(pb.cu_q + i + 1) <= r;
+      behind[k] = i >= pb.batch || __ldg(pb.cu_q + i + 1) > r;
     }
-    int n = 0;
+    int first = 128;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) n += __popc(__ballot_sync(0xffffffffu, done[k]));
-    b += n;
-    if (n < 128) break;
+    for (int k = 3; k >= 0; --k) {
+      const uint32_t any = __ballot_sync(0xffffffffu, behind[k]);
+      if (any != 0) first = 32 * k + __ffs((int)any) - 1;
+    }
+    if (first < 128) return min(base + first, pb.batch);
   }
-  return b;
+  return pb.batch;
+}
+
+// The tables' entries of sequence s; false where they are out of range (its
+// rows do not rise within the M there are, or its length has no room in the
+// block table).
+__device__ __forceinline__ bool sequence_entries(const PagedBatch& pb, int s, int& c0, int& c1,
+                                                 int& len) {
+  c0 = __ldg(pb.cu_q + s);
+  c1 = __ldg(pb.cu_q + s + 1);
+  len = __ldg(pb.kv_len + s);
+  return c0 >= 0 && c1 >= c0 && c1 <= pb.M && len >= 0 &&
+         len <= pb.stride * pb.page_size;            // at most 2^30
 }
 
 template <bool BF16>
@@ -171,14 +184,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p)
 
   grid_launch_dependents();
   grid_dependency_wait();
-  if (r >= p.pb.M) return;
 
   const char* qrow = reinterpret_cast<const char*>(p.Q) + (long long)r * p.ldq * ESZ;
   const char* krow = reinterpret_cast<const char*>(p.K) + (long long)r * p.ldk * ESZ;
   const char* vrow = reinterpret_cast<const char*>(p.V) + (long long)r * p.ldv * ESZ;
   auto load = [&](int h, uint4& x, uint4& y) {
     x = y = make_uint4(0, 0, 0, 0);
-    if (h >= heads || !active) return;
+    if (h >= heads || !active || r >= p.pb.M) return;
     const char* base = h < p.qh           ? qrow + h * D * ESZ
                        : h < p.qh + p.kvh ? krow + (h - p.qh) * D * ESZ
                                           : vrow + (h - p.qh - p.kvh) * D * ESZ;
@@ -189,16 +201,26 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p)
 #pragma unroll
   for (int k = 0; k < kRopeDepth; ++k) load(h0 + k * step, a[k], b[k]);
 
+  // ---- the tables: each sequence is looked at once, whether or not a row is
+  // found to be its own (beside the loads above and the look-up below)
+  for (long long s = (long long)blockIdx.x * kRopeThreads + threadIdx.x; s < p.pb.batch;
+       s += (long long)gridDim.x * kRopeThreads) {
+    int c0, c1, len;
+    if (!sequence_entries(p.pb, (int)s, c0, c1, len)) record_device_error(DEV_ERR_INDEX);
+  }
+  if (r >= p.pb.M) return;
+
   // ---- the token's place
   int pos;
   long long dst = -1;                            // first element of its head 0 in the cache
   {
     const int s = sequence_of(p.pb, r, lane);
     if (s >= p.pb.batch) return;                 // behind the last sequence
-    const int c0 = __ldg(p.pb.cu_q + s), c1 = __ldg(p.pb.cu_q + s + 1);
-    pos = __ldg(p.pb.kv_len + s) - (c1 - r);
-    // c0 > r only in a table of rows that does not rise
-    if (pos < 0 || r < c0) return;
+    int c0, c1, len;
+    // r < c0 or r >= c1 only in a table of rows that does not rise
+    if (!sequence_entries(p.pb, s, c0, c1, len) || r < c0 || r >= c1) return;
+    pos = len - (c1 - r);
+    if (pos < 0) return;
     const int at = pos / p.pb.page_size;
     int page = -1;
     if (at < p.pb.stride) page = __ldg(p.pb.table + (long long)s * p.pb.stride + at);

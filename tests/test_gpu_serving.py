@@ -419,6 +419,51 @@ def test_rope_append_reports_pages_out_of_range():
     assert bn.bitnet_check_device_error() == bn.BITNET_OK
 
 
+BAD_TABLES = [
+    # lengths, cu_q, kv_len, sequences whose tokens are still appended
+    ([(4, 40), (3, 10)], None, [-5, 10], [1]),
+    ([(4, 40), (3, 10)], None, [40, 400000], [0]),
+    ([(4, 40), (3, 10)], [0, 4, 14], None, [0]),
+    ([(7, 40)], [0, 14], None, []),
+    ([(7, 40)], [4, 2], None, []),
+    ([(7, 40)], [-3, 7], None, []),
+    ([(4, 40), (3, 10)], [0, 7, 4], None, [0]),
+    ([(7, 40), (0, 10)], None, [40, -1], [0]),          # no row names that sequence
+    ([(7, 40), (0, 10)], [0, 7, 9], None, [0]),
+    ([(1, 5)] * 500 + [(0, 1)], None, [5] * 500 + [-1], range(500)),
+]
+
+
+@pytest.mark.parametrize("lens,cu,kv,good", BAD_TABLES, ids=range(len(BAD_TABLES)))
+def test_rope_append_reports_rows_and_lengths_out_of_range(lens, cu, kv, good):
+    """A sequence whose rows or length are out of range leaves the cache as it is, and is recorded,
+    as the attention over the same tables does."""
+    s = ref.batch(lens, 16, 2, 64, seed=4)
+    M, g = s["M"], s["g"]
+    q, k, v = (torch.randn(M, h * 64, generator=g).to(BF).cuda() for h in (8, 2, 2))
+    d = cuda(s)
+    kc, vc = d["kc"].clone(), d["vc"].clone()
+    if cu is not None:
+        d["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    if kv is not None:
+        d["len"] = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    bn.bitnet_rope_append(q, k, v, torch.rand(32, generator=g).cuda(), d["cu"], d["len"],
+                          d["table"], d["kc"], d["vc"], torch.empty_like(q))
+    assert bn.bitnet_check_device_error() == bn.BITNET_ERR_INVALID_ARG
+    at, ln = d["cu"].tolist(), d["len"].tolist()
+    slots = set()
+    for b in good:
+        for pos in range(ln[b] - (at[b + 1] - at[b]), ln[b]):
+            slots.add((int(s["table"][b, pos // 16]), pos % 16))
+    for now, before in ((d["kc"], kc), (d["vc"], vc)):
+        changed = (now != before).any(dim=-1).any(dim=1).nonzero().tolist()
+        assert {tuple(c) for c in changed} == slots
+    ws = bn.alloc_attention_workspace(M, len(lens), 8, 2, 64)
+    bn.bitnet_attention(q, d["cu"], d["len"], d["table"], d["kc"], d["vc"], torch.empty_like(q), ws)
+    assert bn.bitnet_check_device_error() == bn.BITNET_ERR_INVALID_ARG
+    assert bn.bitnet_check_device_error() == bn.BITNET_OK
+
+
 def test_binding_refuses_wrong_tensors():
     """Types, shapes, layouts and devices are checked before anything is launched."""
     s = ref.batch([(2, 20), (1, 9)], 16, 2, 64, seed=1)
