@@ -325,7 +325,10 @@ def _paged(cu_q, kv_len, block_table, k_cache, v_cache):
 def bitnet_linear_w8(Xq, x_scale, Wq, w_scale, Y, silu=False, residual=None, epilogue=None,
                      stream=None):
     """Y [M][N] = (Xq . Wq^T) / (x_scale[m] w_scale[n]) (int32 Y: the sum itself), the codes
-    and scales of both sides from bitnet_quant_act (see include/bitnet.h)."""
+    and scales of both sides from bitnet_quant_act (see include/bitnet.h).  An explicit epilogue
+    names the type and all of the flags, those of silu and residual too."""
+    if silu and epilogue is not None and not epilogue & BITNET_EPI_SILU:
+        raise ValueError("silu=True, but the epilogue does not have BITNET_EPI_SILU")
     index = _current_device()
     xq, xs, wq, ws, y = _device_ptrs("Xq x_scale Wq w_scale Y", index, Xq, x_scale, Wq, w_scale, Y)
     if not (Xq.dim() == 2 and Wq.dim() == 2 and Xq.dtype == Wq.dtype == torch.int8):

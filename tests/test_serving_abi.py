@@ -114,6 +114,21 @@ def test_binding_refuses_host_tensors():
         bn.bitnet_rope_append(t, t, t, t[0], i, i[:1], i[None], c, c, t)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(epilogue=bn.BITNET_F32),
+    dict(epilogue=bn.BITNET_F32 | bn.BITNET_EPI_RESIDUAL, residual=torch.zeros(4, 8)),
+])
+def test_linear_w8_refuses_a_silu_that_the_epilogue_leaves_out(kw):
+    """The flags of an explicit epilogue are all that the call takes: a SiLU asked for beside one
+    without it would be left out silently.  (A residual without its flag, or the flag without a
+    residual, is refused by the library.)"""
+    q, s = torch.zeros((4, 64), dtype=torch.int8), torch.ones(4)
+    kw["silu"] = True
+    with pytest.raises(ValueError, match="silu"):
+        bn.bitnet_linear_w8(q, s, torch.zeros((8, 64), dtype=torch.int8), torch.ones(8),
+                            torch.zeros(4, 8), **kw)
+
+
 # ------------------------------------------------------ the references' own pins
 
 def test_reference_attention_by_hand():
