@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(AttnParams p) {
   const int wr = WR == 4 ? warp : 0, wk = WR == 4 ? 0 : warp;
   const int D = p.D, chunks = D / 8;
 
+  grid_dependency_wait();                        // in this order: see rope_append_kernel
   grid_launch_dependents();
-  grid_dependency_wait();
   make_plan(p, plan);
 
   for (long long c = blockIdx.x;; c += gridDim.x) {
@@ -870,8 +870,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnParams p) {
   __shared__ float s_o[4][kRopeMaxDim];
   __shared__ float s_ml[4][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_wait();                        // in this order: see rope_append_kernel
   grid_launch_dependents();
-  grid_dependency_wait();
   const long long share = p.plan[0], total = p.plan[2];
   const int align = (int)p.plan[1];
   const int c = blockIdx.x;

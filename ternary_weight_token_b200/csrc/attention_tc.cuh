@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependency_wait();                        // in this order: see rope_append_kernel
   grid_launch_dependents();
-  grid_dependency_wait();
   const uint32_t tbase = *tmem_slot;
   make_plan(p, plan);
 

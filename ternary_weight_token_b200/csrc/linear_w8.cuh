@@ -158,8 +158,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependency_wait();                        // in this order: see rope_append_kernel
   grid_launch_dependents();
-  grid_dependency_wait();
   const uint32_t tbase = *tmem_slot;
 
   if (warp == 0) {

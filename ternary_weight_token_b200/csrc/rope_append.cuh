@@ -182,8 +182,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p)
   int e0, e1;
   rope_runs(active ? j : 0, N, p, e0, e1);
 
-  grid_launch_dependents();
+  // the next launch may start only once the work before this one has completed:
+  // one that reads inputs early then never looks past the launch before it
   grid_dependency_wait();
+  grid_launch_dependents();
 
   const char* qrow = reinterpret_cast<const char*>(p.Q) + (long long)r * p.ldq * ESZ;
   const char* krow = reinterpret_cast<const char*>(p.K) + (long long)r * p.ldk * ESZ;

@@ -650,3 +650,60 @@ def test_decode_step_of_a_block(new):
     finish()
     torch.cuda.synchronize()
     assert torch.equal(o, first[0]) and torch.equal(logits, first[1])
+
+
+@pytest.mark.parametrize("between", ["append", "attention", "linear_w8"])
+@pytest.mark.parametrize("M", [1, 5, 16])
+def test_early_reading_calls_look_past_one_launch_at_most(M, between):
+    """bitnet_linear with BITNET_LAUNCH_PDL_INPUTS reads its inputs while the launch before it runs.
+    That launch may be one of the serving calls, which does not write them, behind the quantiser
+    or the packing that does: each round has other activations and other weights."""
+    K, N, rounds = 6912, 2560, 12
+    g = torch.Generator().manual_seed(40 + M)
+    W = [(torch.randn(N, K, generator=g) * 0.02).cuda() for _ in range(2)]
+    X = (torch.randn(rounds, M, K, generator=g) * 3).cuda()
+    s = ref.batch([(1, 70)] * M, 16, 5, 128, seed=41)
+    d = cuda(s)
+    q, k, v = (torch.randn(M, h * 128, generator=g).to(BF).cuda() for h in (20, 5, 5))
+    qo, o = torch.empty_like(q), torch.empty_like(q)
+    inv = torch.rand(64, generator=g).cuda()
+    aws = bn.alloc_attention_workspace(M, M, 20, 5, 128)
+    wq = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8).cuda()
+    wsc, other = torch.rand(N, generator=g).cuda() + 1, torch.empty(M, N, device="cuda")
+    P, gamma, pws = bn.alloc_packed(N, K)
+    xq, xs, xr = bn.alloc_quant(M, K)
+    xq2, xs2, _ = bn.alloc_quant(M, K)
+    bn.bitnet_quant_act(X[0], xq2, xs2)
+
+    def middle():
+        if between == "append":
+            bn.bitnet_rope_append(q, k, v, inv, d["cu"], d["len"], d["table"], d["kc"], d["vc"], qo)
+        elif between == "attention":
+            bn.bitnet_attention(q, d["cu"], d["len"], d["table"], d["kc"], d["vc"], o, aws)
+        else:
+            bn.bitnet_linear_w8(xq2, xs2, wq, wsc, other)
+
+    def steps(flags, wait):
+        out = torch.empty(rounds, 2, M, N, device="cuda")
+        for i in range(rounds):
+            bn.bitnet_pack_weights(W[i % 2], P, gamma, pws)
+            wait()
+            bn.bitnet_quant_act(X[i], xq, xs, xr)
+            wait()
+            middle()
+            wait()
+            bn.bitnet_linear(xq, xs, xr, P, gamma, K, out[i, 0], epilogue=bn.BITNET_F32 | flags)
+            wait()
+            bn.bitnet_pack_weights(W[1 - i % 2], P, gamma, pws)
+            wait()
+            middle()
+            wait()
+            bn.bitnet_linear(xq, xs, xr, P, gamma, K, out[i, 1], epilogue=bn.BITNET_F32 | flags)
+            wait()
+        torch.cuda.synchronize()
+        assert bn.bitnet_check_device_error() == bn.BITNET_OK
+        return out
+
+    want = steps(0, torch.cuda.synchronize)
+    for flags in (bn.BITNET_LAUNCH_PDL, bn.BITNET_LAUNCH_PDL_INPUTS):
+        assert torch.equal(steps(flags, lambda: None), want)
