@@ -145,7 +145,8 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float* x) {
 // First element of the two runs of N that lane slot j of a head holds: runs of
 // pairs (first[i], second[i]) when the pairs are split in halves, one run of
 // 2 N elements when they are interleaved.  Past the rotated part the rest of
-// the head is paired the same way, at angle zero.
+// the head is paired the same way, and is not turned; rot / 2 is a multiple of
+// 8, so a slot lies on one side.
 __device__ __forceinline__ void rope_runs(int j, int n, const RopeParams& p, int& e0, int& e1) {
   if (p.interleaved) {
     e0 = 2 * n * j;
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p)
   while (width < lanes) width *= 2;
   const int j = lane & (width - 1);
   const bool active = j < lanes;
+  const bool turned = N * j < p.rot / 2;         // the slot's pairs are rotated
   const int slots = 32 / width;                  // heads of a warp at a time
   const int heads = p.qh + 2 * p.kvh;
   const int gw = blockIdx.x * (kRopeThreads / 32) + warp;
@@ -280,7 +282,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeParams p)
           x[N + i] = x[N + i] * rr * (g ? __ldg(g + e1 + i) : 1.0f);
         }
       }
-      if (p.interleaved) {
+      if (!turned) {
+        // passes as it is: 0 times an infinity is not 0
+      } else if (p.interleaved) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float u = x[2 * i], v = x[2 * i + 1];

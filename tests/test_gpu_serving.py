@@ -403,6 +403,37 @@ def test_rope_append_in_place_and_without_a_place():
     close(d["kc"], kc, ktol, "k cache")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [0, 32])
+def test_rope_append_passes_the_rest_of_a_head_as_it_is(rot, interleaved, dtype):
+    """Elements past rot_dim keep their bits, infinities and negative zeros too."""
+    qh, kvh, D, M = 4, 2, 96, 5
+    s = ref.batch([(M, 20)], 16, kvh, D, seed=14)
+    g = s["g"]
+    q, k, v = (torch.randn(M, h, D, generator=g) for h in (qh, kvh, kvh))
+    for x in (q, k):
+        x[..., rot:].masked_fill_(torch.rand(M, x.shape[1], D - rot, generator=g) < 0.2, -0.0)
+        x[..., rot:].masked_fill_(torch.rand(M, x.shape[1], D - rot, generator=g) < 0.2,
+                                  float("inf"))
+        x[..., rot:].masked_fill_(torch.rand(M, x.shape[1], D - rot, generator=g) < 0.2,
+                                  -float("inf"))
+    q, k, v = (x.to(dtype).cuda() for x in (q, k, v))
+    d, out = cuda(s), torch.empty(M, qh * D, dtype=dtype, device="cuda")
+    inv = torch.rand(rot // 2, generator=g).cuda()
+    bn.bitnet_rope_append(q.view(M, -1), k.view(M, -1), v.view(M, -1), inv, d["cu"], d["len"],
+                          d["table"], d["kc"], d["vc"], out, rope=int(interleaved))
+    assert bn.bitnet_check_device_error() == bn.BITNET_OK
+
+    def bits(x):
+        return x.contiguous().view(torch.int16 if x.dtype == BF else torch.int32)
+    assert torch.equal(bits(out.view(M, qh, D)[..., rot:]), bits(q[..., rot:]))
+    pos = torch.arange(15, 20, device="cuda")
+    now = d["kc"][d["table"][0].long()[pos // 16], :, pos % 16]
+    assert torch.equal(bits(now[..., rot:]), bits(k[..., rot:].to(BF)))
+    assert torch.isfinite(out.view(M, qh, D)[..., :rot]).all()
+
+
 def test_rope_append_reports_pages_out_of_range():
     s = ref.batch([(4, 40), (1, 10)], 16, 2, 64, seed=4)
     q, k, v = (torch.randn(5, h * 64, generator=s["g"]).to(BF).cuda() for h in (8, 2, 2))
