@@ -305,8 +305,9 @@ BITNET_API int bitnet_linear_w8(const int8_t *Xq, const float *x_scale, const in
  *             each head before the rotation, q_gain and k_gain [head_dim] fp32
  *             or NULL for all ones.
  *   Q_out     out: [M][q_heads * head_dim] of `dtype`, contiguous; may be Q
- *             itself when Q's rows are.  Rows without a place keep their
- *             contents.  Keys and values are rounded to bf16 once.
+ *             itself when Q's rows are, and overlaps nothing else of Q, K and
+ *             V.  Rows without a place keep their contents.  Keys and values
+ *             are rounded to bf16 once.
  * The slots appended to must be distinct.  Errors: INVALID_ARG, CUDA. */
 BITNET_API int bitnet_rope_append(const void *Q, int64_t q_stride, const void *K,
                                   int64_t k_stride, const void *V, int64_t v_stride, int dtype,

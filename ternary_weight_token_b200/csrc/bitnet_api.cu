@@ -868,6 +868,16 @@ int validate_paged(int dtype, int M, int q_heads, int kv_heads, int head_dim, in
   return BITNET_OK;
 }
 
+// Whether the `bytes` at `out` meet one of M rows of `row` bytes, `stride` bytes
+// apart (row <= stride), from `base`.
+bool meets_rows(const void* out, long long bytes, const void* base, long long row,
+                long long stride, int M) {
+  const long long lo = (long long)(reinterpret_cast<uintptr_t>(out) -
+                                   reinterpret_cast<uintptr_t>(base));
+  const long long r = lo < row ? 0 : (lo - row) / stride + 1;   // first row that ends behind out
+  return r < M && r * stride < lo + bytes;
+}
+
 // Kernel and row tile of an attention call (pure host logic).
 struct AttnShape {
   bool tc;                             // tensor-core kernel
@@ -1580,6 +1590,11 @@ int bitnet_rope_append(const void* Q, int64_t q_stride, const void* K, int64_t k
       return fail(BITNET_ERR_INVALID_ARG, "tables and gains must be 4-byte aligned");
   if (Q_out == Q && q_stride != wq)
     return fail(BITNET_ERR_INVALID_ARG, "in place (Q_out == Q) needs contiguous query rows");
+  const int size = dtype == BITNET_BF16 ? 2 : 4;
+  if ((Q_out != Q && meets_rows(Q_out, M * wq * size, Q, wq * size, q_stride * size, M)) ||
+      meets_rows(Q_out, M * wq * size, K, wk * size, k_stride * size, M) ||
+      meets_rows(Q_out, M * wq * size, V, wk * size, v_stride * size, M))
+    return fail(BITNET_ERR_INVALID_ARG, "Q_out must not overlap K, V or a part of Q");
   DeviceInfo di;
   if (int rc = device_info(di)) return rc;
   RopeParams p = {};
@@ -1639,7 +1654,9 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   for (const void* q : words)
     if (reinterpret_cast<uintptr_t>(q) & 3u)
       return fail(BITNET_ERR_INVALID_ARG, "tables must be 4-byte aligned");
-  if (O == Q) return fail(BITNET_ERR_INVALID_ARG, "O must not be Q's buffer");
+  const long long row = (long long)q_heads * head_dim * (dtype == BITNET_BF16 ? 2 : 4);
+  if (meets_rows(O, M * row, Q, row, row, M))
+    return fail(BITNET_ERR_INVALID_ARG, "O must not overlap Q's buffer");
   const size_t ws_need = bitnet_attention_workspace_size(M, batch, q_heads, kv_heads, head_dim);
   if (workspace == nullptr || ws_bytes < ws_need)
     return fail(BITNET_ERR_WORKSPACE, "workspace of %zu bytes needed", ws_need);

@@ -434,6 +434,28 @@ def test_rope_append_passes_the_rest_of_a_head_as_it_is(rot, interleaved, dtype)
     assert torch.isfinite(out.view(M, qh, D)[..., :rot]).all()
 
 
+def test_outputs_beside_the_inputs_in_one_buffer():
+    """Neighbours, and an output between the rows of its inputs, are no overlap."""
+    M, qh, kvh, D = 3, 4, 2, 64
+    s = ref.batch([(M, 40)], 16, kvh, D, seed=15)
+    g = s["g"]
+    rows = torch.randn(M, 8192, generator=g).to(BF).cuda()      # q, k, v and room per row
+    q, k, v = rows[:, :256], rows[:, 256:384], rows[:, 384:512]
+    spare = rows.view(-1)[512:512 + M * 256].view(M, 256)
+    inv = torch.rand(32, generator=g).cuda()
+    d, e = cuda(s), cuda(s)
+    apart = torch.empty(M, 256, dtype=BF, device="cuda")
+    bn.bitnet_rope_append(q, k, v, inv, d["cu"], d["len"], d["table"], d["kc"], d["vc"], apart)
+    bn.bitnet_rope_append(q, k, v, inv, e["cu"], e["len"], e["table"], e["kc"], e["vc"], spare)
+    assert torch.equal(spare, apart) and torch.equal(d["kc"], e["kc"])
+    both = torch.empty(2 * M, 256, dtype=BF, device="cuda")
+    both[:M] = apart
+    ws = bn.alloc_attention_workspace(M, 1, qh, kvh, D)
+    bn.bitnet_attention(both[:M], d["cu"], d["len"], d["table"], d["kc"], d["vc"], both[M:], ws)
+    assert torch.equal(both[:M], apart)
+    assert torch.equal(both[M:], run_attention({**s, "kc": d["kc"], "vc": d["vc"]}, apart, qh))
+
+
 def test_rope_append_reports_pages_out_of_range():
     s = ref.batch([(4, 40), (1, 10)], 16, 2, 64, seed=4)
     q, k, v = (torch.randn(5, h * 64, generator=s["g"]).to(BF).cuda() for h in (8, 2, 2))

@@ -93,6 +93,28 @@ def test_attention_refuses_the_queries_buffer_as_output():
     assert "buffer" in bn.bitnet_last_error()
 
 
+@pytest.mark.parametrize("at", [0x10000 + 16, 0x10000 - 16, 0x10000 + 4 * 1024 - 16,
+                                0x10000 - 4 * 1024 + 16])
+def test_attention_refuses_outputs_that_overlap_the_queries(at):
+    """4 rows of 1024 bytes on each side: every row is read while others are written."""
+    assert attend(out=ctypes.c_void_p(at)) == INVALID
+    assert "overlap" in bn.bitnet_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(Q=0x20000 + 16), dict(Q=0x20000 - 16), dict(K=0x20000), dict(V=0x20000 + 4080),
+    dict(K=0x20000 - 256 * 4 + 16), dict(V=0x20000 - 256 * 4 + 16),
+    # rows 4096 bytes apart (2048 elements): the output lies between two, and reaches the next
+    dict(Q=0x20000 - 1024, ldq=2048, K=0x20000 - 256 + 16, ldk=2048),
+    dict(V=0x20000 - 3072, ldv=2048),
+])
+def test_rope_append_refuses_outputs_that_overlap_its_inputs(kw):
+    """Output of 4 rows of 1024 bytes at 0x20000; keys and values have rows of 256 bytes."""
+    kw = {k: ctypes.c_void_p(v) if k in "QKV" else v for k, v in kw.items()}
+    assert append(**kw) == INVALID
+    assert "overlap" in bn.bitnet_last_error()
+
+
 def test_attention_workspace_serves_smaller_calls():
     size = bn.bitnet_attention_workspace_size
     for qh, kvh, D in ((20, 5, 128), (8, 8, 64), (4, 2, 256), (20, 1, 96)):
