@@ -119,3 +119,66 @@ def linear_w8(xq, xs, wq, ws, silu=False, residual=None):
     if residual is not None:
         y = y + residual.double()
     return acc.to(torch.int64), y
+
+
+# ------------------------------------------------- inputs that show single steps
+
+def one_key_scores(lens, page, qh, kvh, D, lo, hi, seed=0):
+    """A paged batch and fp32 queries whose rows weigh two keys: position 0 with score 0 and value
+    0, position 1 with a score z in [-hi, -lo] of 24 bits and value 1; the rest score -120 (weight
+    2^-173) with value 0.  So o = 2^x / (1 + 2^x), x = z log2 e, in every element, each score is one
+    product, and a term of q or of the probability that is left out shows at its full size.
+    Returns (batch, q, z [M][qh]); rows before position 1 have o = 0."""
+    s = batch(lens, page, kvh, D, seed=seed, fill=float("nan"))
+    s["kc"].zero_()
+    s["vc"].zero_()
+    for b, (_, t) in enumerate(lens):
+        used = s["table"][b, :-(-t // page)].long()
+        s["kc"][used, :, :, 1] = 1.0
+        s["kc"][used[0], :, 0, 1] = 0.0
+        if t > 1:
+            at = (used[1 // page], slice(None), 1 % page)
+            s["kc"][at] = 0.0
+            s["kc"][(*at, 0)] = 1.0
+            s["vc"][at] = 1.0
+    z = -(lo + (hi - lo) * torch.rand(s["M"], qh, generator=s["g"]))
+    q = torch.zeros(s["M"], qh, D)
+    q[..., 0], q[..., 1] = z, -120.0
+    return s, q.view(s["M"], -1), z.double()
+
+
+def one_key_tolerance(z):
+    """Relative bound on o, in units of 2^-24.  z: its three products are added with a truncation
+    of 2^-23 each (6), the factor and the product with it are rounded and so is the difference to
+    the maximum (3).  p: exp2 within 2^-22 (4), the three products with v truncated (6), its own
+    24 bits, the sums, the reciprocal and the last product (8)."""
+    return (z.abs() * 9 + 18) * 2.0 ** -24
+
+
+def terms(x, n):
+    """What n bf16 terms of fp32 values hold."""
+    x, out = x.float(), torch.zeros_like(x, dtype=torch.float64)
+    for _ in range(n):
+        t = x.to(BF).float()
+        out += t.double()
+        x = x - t
+    return out
+
+
+def block_counts(lens, page, kvh, D, seed=0):
+    """A paged batch for queries of zeros: every key weighs the same, and the value of position j
+    is 1 in channel (j // 64) % D.  So a row at position p has o[d] = (its positions of channel d)
+    / (p + 1) with sums of whole numbers, and a block lost, doubled or taken from another page
+    shows.  Returns (batch, o [M][D] in 64 bits)."""
+    s = batch(lens, page, kvh, D, seed=seed, fill=float("nan"))
+    rows = []
+    for b, (n, t) in enumerate(lens):
+        j = torch.arange(t)
+        hot = torch.zeros(t, D, dtype=torch.float64)
+        hot[j, (j // 64) % D] = 1.0
+        if t:
+            s["vc"][s["table"][b].long()[j // page], :, j % page] = hot[:, None].to(BF)
+        upto = torch.cat([torch.zeros(1, D, dtype=torch.float64), hot.cumsum(0)])
+        p1 = (t - n + torch.arange(n) + 1).clamp(min=0)
+        rows.append(upto[p1] / p1.clamp(min=1)[:, None])
+    return s, torch.cat(rows)

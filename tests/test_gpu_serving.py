@@ -171,6 +171,57 @@ def test_attention_cut_items_repeat_bit_for_bit(case):
     assert not other, f"runs {other} differ from the first"
 
 
+ONE_KEY = [([(1, 300), (1, 2)], 20, 5, 128, 16), ([(1, 715)], 8, 1, 64, 64),   # 8 rows, 8 heads
+           ([(3, 500), (2, 40)], 20, 5, 128, 16), ([(2, 90)], 8, 1, 256, 16),  # 16 rows
+           ([(128, 128), (70, 333)], 8, 8, 64, 16), ([(40, 1000)], 20, 5, 128, 32),
+           ([(1, 9000)], 20, 5, 128, 128), ([(33, 6000)], 4, 2, 96, 48)]
+
+
+@pytest.mark.parametrize("lo,hi", [(4, 12), (0.25, 3)])
+@pytest.mark.parametrize("case", ONE_KEY, ids=str)
+def test_attention_fp32_holds_queries_and_probabilities_in_24_bits(case, lo, hi):
+    """Two terms of q or of p in place of three pass the bound three times over (a CPU test of the
+    bound shows it)."""
+    lens, qh, kvh, D, page = case
+    s, q, z = ref.one_key_scores(lens, page, qh, kvh, D, lo, hi, seed=50)
+    got = run_attention(s, q.cuda(), qh, scale=1.0).double().cpu().view(s["M"], qh, D)
+    pos = torch.cat([torch.arange(t - n, t) for n, t in lens])
+    want = torch.where(pos[:, None] >= 1, torch.sigmoid(z), torch.zeros_like(z))[..., None]
+    close(got, want.expand(-1, -1, D),
+          (want * ref.one_key_tolerance(z)[..., None]).expand(-1, -1, D) + 1e-30, "one key")
+
+
+COUNTS = [
+    ([(1, 70001), (1, 3000)], 20, 5, 128, 128),
+    ([(1, 1 + (i * 911) % 2500) for i in range(300)] + [(1, 30000)], 4, 1, 64, 32),
+    ([(2, 1000), (1, 64), (1, 1), (2, 65), (1, 4097)], 20, 5, 128, 16),
+    ([(1, 90), (1, 17), (1, 3001)], 6, 6, 80, 112),
+    ([(4, 130), (4, 7000)], 4, 2, 256, 16),
+    ([(300, 9000)], 20, 5, 128, 64),
+    ([(300, 9000), (2, 2), (40, 0), (40, 3000), (130, 5000)], 20, 5, 128, 32),
+    ([(33, 20000), (1, 30), (257, 4100)], 6, 2, 128, 16),
+    ([(257, 9001), (64, 64), (500, 6100)], 12, 4, 96, 48),
+    ([(40, 20011)], 8, 8, 64, 32),
+    ([(130, 9000)], 8, 2, 128, 128),
+    ([(700, 700), (257, 1300)], 20, 5, 128, 64),
+    ([(21, 2050)], 2, 1, 256, 16),
+    ([(1500, 1500)] + [(1, 1 + i % 9) for i in range(60)], 64, 64, 64, 16),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("case", COUNTS, ids=[str(c)[:60] for c in COUNTS])
+def test_attention_counts_every_block_once(case, dtype):
+    """Equal weights over one-hot values: sums are whole numbers, so what is left is the quotient's
+    two roundings (2^-24 each, and one for the reciprocal) and the output's."""
+    lens, qh, kvh, D, page = case
+    s, want = ref.block_counts(lens, page, kvh, D, seed=60)
+    q = torch.zeros(s["M"], qh * D, dtype=dtype, device="cuda")
+    got = run_attention(s, q, qh).view(s["M"], qh, D)
+    want = want[:, None].expand(-1, qh, -1)
+    close(got, want, want * (3 * 2.0 ** -24 + (2.0 ** -8 if dtype == BF else 0.0)), "counts")
+
+
 def test_attention_ten_new_tokens_each():
     """More than 16 rows a sequence, all in one tile; then 9 to 16 rows."""
     check_attention([(10, 500)] * 7, 20, 5, 128, 16, BF)

@@ -181,3 +181,35 @@ def test_reference_rope_by_hand():
              ref.rope(b, 1, 16, torch.tensor([p + 7]), f, False, False, None, 0)[0]).sum()
             for p in (0, 1000)]
     assert torch.allclose(dots[0], dots[1], rtol=1e-9)
+
+
+@pytest.mark.parametrize("lo,hi,what", [(4, 12, "q"), (0.25, 3, "p")])
+def test_one_key_bound_tells_two_terms_from_three(lo, hi, what):
+    """With two bf16 terms of the queries, or of the probabilities, some of 500 rows leave the
+    bound; with three all stay far inside it."""
+    s, q, z = ref.one_key_scores([(100, 130)], 16, 5, 1, 64, lo, hi)
+    o, _, _ = ref.attention(s, q, 5, 1.0)
+    want = torch.sigmoid(z)
+    assert torch.allclose(o.view(100, 5, 64), want[..., None].expand(-1, -1, 64), rtol=1e-12)
+    worst = {}
+    for n in (2, 3):
+        x = ref.terms(z, n) if what == "q" else z
+        p = torch.exp(x)
+        held = ref.terms(p, n) if what == "p" else p
+        worst[n] = ((held / (1 + p) - want).abs() / want / ref.one_key_tolerance(z)).max()
+    assert worst[2] > 3 and worst[3] < 0.1, worst
+
+
+@pytest.mark.parametrize("t", [3000, 70001])
+def test_block_counts_show_a_lost_block(t):
+    """The 64-bit reference gives the counts, and a block of 64 less moves an element by more than
+    the bf16 bound, a single key by more than the fp32 bound."""
+    s, want = ref.block_counts([(2, t)], 128, 1, 128)
+    o, _, _ = ref.attention(s, torch.zeros(2, 128), 1, 1.0)
+    assert torch.allclose(o, want, rtol=1e-12)
+    p = torch.tensor([t - 1, t], dtype=torch.float64)[:, None]
+    count = want * p
+    for lost, bound in ((64, 2.0 ** -8 + 3 * 2.0 ** -24), (1, 3 * 2.0 ** -24)):
+        d = 5                                            # a channel that loses `lost` keys
+        less = (count[:, d] - lost) / (p[:, 0] - lost)
+        assert ((less - want[:, d]).abs() > 2 * want[:, d] * bound).all()
