@@ -268,9 +268,10 @@ BITNET_API int bitnet_linear_multi(const int8_t *Xq, const float *x_scale,
  *   Xq, x_scale   [M][K] codes and [M] scales s = 127 / max|x| of the tokens
  *   Wq, w_scale   [N][K] codes and [N] scales of the output channels
  *   Y         out: [M][N] of the type in (epilogue & BITNET_EPI_TYPE_MASK):
- *             y = acc / (x_scale[m] * w_scale[n]) with the exact int32 sum acc
- *             (three further fp32 roundings), then the optional SiLU and
- *             residual as bitnet_linear(); BITNET_I32 writes acc itself.
+ *             y = acc / (x_scale[m] * w_scale[n]) with the exact int32 sum acc,
+ *             formed in five fp32 roundings (the sum, a reciprocal of each
+ *             scale, their product, the last product), then the optional SiLU
+ *             and residual as bitnet_linear(); BITNET_I32 writes acc itself.
  *   residual  [M][N] of Y's type when BITNET_EPI_RESIDUAL is set, else NULL.
  * Scales must be nonzero.  Y may be residual's buffer.  The launch hints are
  * not taken.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
@@ -294,9 +295,8 @@ BITNET_API int bitnet_linear_w8(const int8_t *Xq, const float *x_scale, const in
  * q_heads is a multiple of kv_heads; query head h reads key/value head
  * h / (q_heads / kv_heads).  head_dim is a multiple of 16 in [16, 256],
  * page_size a multiple of 16, table_stride * page_size and M * q_heads at most
- * 2^30.  The
- * tables are device memory read on the stream, so a captured call follows
- * lengths that change between replays.  A page index, rows (entries of cu_q
+ * 2^30.  The tables are device memory read on the stream, so a captured call
+ * follows lengths that change between replays.  A page index, rows (entries of cu_q
  * that fall or leave 0 .. M) or a length (negative, or more than table_stride *
  * page_size) out of range is recorded in the device error word
  * (bitnet_check_device_error() returns INVALID_ARG); no access is made there
@@ -341,9 +341,11 @@ BITNET_API size_t bitnet_attention_workspace_size(int M, int batch, int q_heads,
  * with none (a negative position) gives zeros.  Scores, softmax statistics and
  * sums are fp32; BF16 calls round the probabilities to bf16 before their
  * product with V, F32 calls carry Q and the probabilities in 24 bits.  Slots
- * past a sequence's length may hold anything, NaN included.  The workspace needs no
- * initialisation; calls that share one must not overlap on the GPU.  O must
- * not overlap Q.  Errors: INVALID_ARG, WORKSPACE, CUDA. */
+ * past a sequence's length may hold anything, NaN included; cached tokens are
+ * inputs and must be finite (a value that is not also reaches earlier new
+ * tokens of its sequence: a weight of 0 times it is not 0).  The workspace
+ * needs no initialisation; calls that share one must not overlap on the GPU.
+ * O must not overlap Q.  Errors: INVALID_ARG, WORKSPACE, CUDA. */
 BITNET_API int bitnet_attention(const void *Q, int dtype, int M, int q_heads, int kv_heads,
                                 int head_dim, float scale, int batch, const int32_t *cu_q,
                                 const int32_t *kv_len, const int32_t *block_table,

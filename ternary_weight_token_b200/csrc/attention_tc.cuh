@@ -15,9 +15,9 @@
 // at most 2^8 and every sum is unchanged in exact arithmetic.
 //
 // Bound by the alternation of softmax and tensor core: a 4096-token prompt of
-// the 2B heads takes 104 us (822 TFLOP/s, tensor pipe active 42 % of the time).
-// A tile's turn is ~1950 cycles for 1024 of products; what it waits for most
-// is the end of the product with V, before the scores may overwrite the
+// the 2B heads takes 103 us (837 TFLOP/s, tensor pipe active 42 % of the time).
+// A tile's turn is ~1930 cycles for 1024 of products; what it waits for most
+// is the end of the product with V (~410), before the scores may overwrite the
 // probabilities that product reads (the architecture orders the two only by
 // completion).
 //
@@ -585,11 +585,16 @@ __global__ void __launch_bounds__(kAttnTcThreads, 1)
       // tensor core works for the other (one issuer for both in turn left it
       // idle half of the time).  The whole warp follows the loop and one
       // elected lane issues, so that descriptors live in uniform registers.
-      // A parity wait may take the phase before for its own if one is skipped, and
-      // misses its own if the barrier gets two ahead.  So every waiter waits in
-      // every phase, and no barrier can complete a phase before all its waiters
-      // have seen the last: slots need both issuers' release, vlast both their
-      // arrivals, the others go to and fro between two sides.
+      // A parity wait takes the phase two before for its own if the one between
+      // is still open, and misses its own if the barrier gets two ahead.  So no
+      // barrier can complete a phase before all its waiters have seen the last:
+      // slots need both issuers' release, vlast both their arrivals, the others
+      // go to and fro between two sides.  Of odone the issuer waits for every
+      // phase but an item's last and the softmax for that one only; each knows
+      // the phase before complete by other means: scores are issued after the
+      // product before them is done, so the softmax that read an item's last
+      // scores waits in the open phase, and queries are handed over after the
+      // softmax saw the last item's end, so the issuer that got them does.
       const int cnt = t == 0 ? job.cnt[0] : job.cnt[1];
       const uint32_t q_phase = t == 0 ? tiles_done[0] : tiles_done[1];
       bool ok = true;

@@ -893,9 +893,19 @@ AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, 
   // kernel's pairs of 128-row tiles for bf16; its softmax wants a positive
   // scale.  What is left takes tiles of 64, heads wider than 128 (no registers
   // for 64) of 16.
+  // Small tiles / tensor cores, 2B heads (4 rows a token): 16 sequences over
+  // 1500 keys of 4 new tokens 31 / 41 us, of 5 42 / 41, of 8 44 / 40; 64 decodes
+  // over 1000 keys and a chunk of 190 tokens 77 / 89 us, of 512 133 / 89.
   const long long rows = (long long)M * G;
   const bool few = rows <= 16ll * batch;
   sh.tc = !few && !f32 && head_dim <= 128 && scale > 0.0f;
+  // Smallest shares: smaller ones cost more in the join than they bring.  Tensor
+  // cores, 2 / 3 / 4 / 6 blocks: 130 tokens over 9000 keys of two heads 50.5 / 41.8
+  // / 39.2 / 38.9 us, three chunks of 64 over 4096 42.7 / 42.6 / 32.7 / 35.3.  Small
+  // tiles, 1 / 2 / 4: one token over 715 keys 10.3 / 10.7 / 11.6 us, two sequences
+  // of 3 over 1500 17.4 / 15.8 / 16.2.  Tiles of 64 (fp32), 4 / 8 / 16: eight
+  // prompts of 128 58.6 / 44.0 / 44.0 us, three chunks of 40 over 1000 39.4 / 38.1 /
+  // 63.0.
   if (sh.tc) {
     sh.rt_shift = 8;
     sh.unit_shift = 7;
@@ -907,8 +917,10 @@ AttnShape attn_shape(int M, int batch, int q_heads, int kv_heads, int head_dim, 
     sh.min_units = sh.rt_shift <= 4 ? 2 : 8;
     sh.target = kAttnTarget;
   }
-  // enough items of chunks to deal out whole, longest first (decode is cut into
-  // equal shares whatever its items: their lengths may differ by any factor)
+  // enough items of chunks to deal out whole (prompt of 4096 tokens 99.8 us, with
+  // the estimate of both forms on the device 103.3; fp32 prompt of 3900 whole 980
+  // us, cut 1427).  Decode is cut into equal shares whatever its items: their
+  // lengths may differ by any factor.
   if (sh.rt_shift > 4 && (rows >> sh.rt_shift) * kv_heads >= 2 * sh.target) sh.target = 0;
   return sh;
 }
@@ -1675,8 +1687,9 @@ int bitnet_attention(const void* Q, int dtype, int M, int q_heads, int kv_heads,
   p.rt_shift = sh.rt_shift; p.unit_shift = sh.unit_shift;
   p.min_keys = sh.min_units << sh.unit_shift; p.target = sh.target;
   // cutting and joining cost the tensor-core kernel about as much as twelve
-  // blocks (one prompt of 3000 tokens: 77 us whole, 113 cut; four chunks over
-  // 1281 - 3782 keys 82.6 / 84.8; two chunks of 1000 over 3000: 95 / 88)
+  // blocks (whole / cut: one prompt of 3000 tokens 76 / 116 us, of 2048 49 / 75,
+  // four prompts of 512 32 / 49; two chunks of 1000 over 3000 95 / 90; chunks of
+  // 140 to 500 over 1281 to 3782 92 / 72)
   p.slack = sh.tc ? 12 * kAttnTcKeys : -1;
   // sequences shorter than the smallest share are not worth cutting
   if ((long long)table_stride * page_size < (long long)sh.min_units << sh.unit_shift) p.target = 0;

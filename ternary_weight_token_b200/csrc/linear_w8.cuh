@@ -99,6 +99,8 @@ __device__ __forceinline__ void w8_store(const uint32_t (&v)[CW], float wf, cons
     }
     T* y = reinterpret_cast<T*>(Y) + at;
     // the sum, two reciprocals, their product and the last product: 2^-24 each
+    // (the quotient itself, three roundings, costs 69 us for 55 at 4096 tokens,
+    // 6912 x 2560; a reciprocal with one correction 59)
     auto value = [&](int j) {
       float x = __fmul_rn(__int2float_rn((int)v[j]), __fmul_rn(wf, tok[j]));
       if constexpr (SILU) x = silu_f32(x);
