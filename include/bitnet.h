@@ -109,13 +109,14 @@ extern "C" {
  * reduction, dequantisation) may then overlap the preceding work; only the
  * writes of Y wait for it to finish.  Ignored for M > 16.
  * Preceding work, for both hints, is all that is not complete when the call in
- * front of this one lets it start.  The quantiser, the serving calls and calls
- * without a hint do so after the work before them is complete, so only that
- * one call counts; calls of 3 to 16 tokens with BITNET_LAUNCH_PDL, the prefill
- * GEMM, bitnet_ffn() and bitnet_pack_weights() do so at their start, so that
- * the work before them counts too.  (Behind quantiser and a hinted 4-token
- * projection, BITNET_LAUNCH_PDL_INPUTS may not read the quantiser's codes:
- * give the first projection no hint, or use bitnet_linear_multi().) */
+ * front of this one lets it start.  The quantiser, the serving calls and decode
+ * calls without a hint do so after the work before them is complete, so only
+ * that one call counts; decode calls with a hint of their own, the prefill
+ * GEMM, bitnet_ffn() and bitnet_pack_weights() may do so at their start, so
+ * that the work before them counts too.  (Behind quantiser and a projection
+ * with BITNET_LAUNCH_PDL, a call with BITNET_LAUNCH_PDL_INPUTS may not read the
+ * quantiser's codes: give the first projection no hint, or use
+ * bitnet_linear_multi().) */
 #define BITNET_LAUNCH_PDL_INPUTS 0x200
 
 /* ----------------------------------------------------------- FFN variants */

@@ -328,6 +328,29 @@ def test_attention_replays_follow_the_lengths():
         close(o2, o, tol, "second graph")
 
 
+def test_attention_calls_in_a_row_share_a_workspace():
+    """Small and cut calls in turn, nothing between them: a call's plan and sums stay until its
+    join has read them."""
+    work, ws_m = [], 0
+    for lens, page, seed in (([(1, 700), (2, 50)], 16, 17), ([(129, 9000), (257, 7000)], 32, 18),
+                             ([(20, 300)], 16, 19)):
+        s = ref.batch(lens, page, 5, 128, seed=seed)
+        q = torch.randn(s["M"], 2560, generator=s["g"]).to(BF).cuda()
+        work.append((cuda(s), q, run_attention(s, q, 20)))
+        ws_m = max(ws_m, s["M"])
+    ws = bn.alloc_attention_workspace(ws_m, 2, 20, 5, 128)
+    outs = [[torch.full_like(q, 7.0) for _, q, _ in work] for _ in range(20)]
+    torch.cuda.synchronize()
+    for row in outs:
+        for (d, q, _), o in zip(work, row):
+            bn.bitnet_attention(q, d["cu"], d["len"], d["table"], d["kc"], d["vc"], o, ws)
+    torch.cuda.synchronize()
+    assert bn.bitnet_check_device_error() == bn.BITNET_OK
+    for row in outs:
+        for (_, _, want), o in zip(work, row):
+            assert torch.equal(o, want)
+
+
 def test_attention_same_bits_twice():
     s = ref.batch([(1, 5000), (3, 900)], 16, 5, 128, seed=8)
     q = torch.randn(4, 2560, generator=s["g"]).to(BF).cuda()
