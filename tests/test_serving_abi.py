@@ -106,7 +106,7 @@ def test_attention_refuses_outputs_that_overlap_the_queries(at):
     dict(K=0x20000 - 256 * 4 + 16), dict(V=0x20000 - 256 * 4 + 16),
     # rows 4096 bytes apart (2048 elements): the output lies between two, and reaches the next
     dict(Q=0x20000 - 1024, ldq=2048, K=0x20000 - 256 + 16, ldk=2048),
-    dict(V=0x20000 - 3072, ldv=2048),
+    dict(V=0x20000 - 2560, ldv=2048),
 ])
 def test_rope_append_refuses_outputs_that_overlap_its_inputs(kw):
     """Output of 4 rows of 1024 bytes at 0x20000; keys and values have rows of 256 bytes."""
